@@ -10,6 +10,9 @@ The calls of the library, one-to-one with include/cvq.h:
   naive_dequant / naive_decode                   -> the comparison path
   encode_append(shape, keys, values, ...)        -> codes written (cvq_encode_append)
   fault_status(clear)                            -> device fault bits (cvq_fault_status)
+  prefix_attend(shape, q, key_cb, codes...)      -> (out, lse)   (cvq_prefix_attend)
+  paged_append(paged, k, v, ...)                 -> rotated q    (cvq_paged_append)
+  paged_attend(paged, q, k_pages, v_pages, ...)  -> (out, lse)   (cvq_paged_attend)
 
 plus attend(), which allocates the intermediate buffers with torch and runs the calls in
 order.  Tensors are torch CUDA tensors in the layouts documented in cvq.h; work is
@@ -28,7 +31,9 @@ from ._binding import CVQ_BF16, CVQ_F32, CvqError, cvq_shape, make_shape  # noqa
 __all__ = ["make_shape", "shape_of", "qtable", "decode_attn", "decode_attn_gqa", "combine",
            "attend", "naive_dequant", "naive_decode", "encode_append", "split_tokens",
            "suggest_splits", "partials_alloc", "group_dim_of", "attend_fused", "workspace_alloc",
-           "fault_status", "CvqError"]
+           "fault_status", "CvqError", "prefix_attend", "prefix_suggest_splits",
+           "prefix_workspace_alloc", "make_paged", "paged_append", "paged_attend",
+           "paged_suggest_splits", "paged_workspace_alloc"]
 
 
 def _ptr(t):
@@ -337,3 +342,8 @@ def attend(q, key_cb, val_cb, key_codes, val_codes, seq_lens, rope_base=500000.0
     else:
         raise ValueError(form)
     return combine(shape, n_splits, *parts, stream=stream)
+
+
+from .serving import (make_paged, paged_append, paged_attend, paged_suggest_splits,  # noqa: E402
+                      paged_workspace_alloc, prefix_attend, prefix_suggest_splits,
+                      prefix_workspace_alloc)

@@ -17,6 +17,7 @@ LIB_PATH = os.path.join(PKG, "libcvq_debug.so" if os.environ.get("CVQ_LIBRARY") 
 CVQ_OK = 0
 CVQ_F32 = 0
 CVQ_BF16 = 1
+CVQ_F16 = 2              # shared-prefix and paged calls only
 STATUS_NAMES = {0: "CVQ_OK", 1: "CVQ_ERR_NULL", 2: "CVQ_ERR_SHAPE", 3: "CVQ_ERR_ALIGN",
                 4: "CVQ_ERR_UNSUPPORTED", 5: "CVQ_ERR_WORKSPACE", 6: "CVQ_ERR_CUDA",
                 7: "CVQ_ERR_STATIC_LIMIT"}
@@ -35,13 +36,21 @@ class cvq_shape(ctypes.Structure):
                 ("group_dim", ctypes.c_int32), ("code_bits", ctypes.c_int32)]
 
 
+class cvq_paged(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("n_q_heads", ctypes.c_int32),
+                ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("n_pages", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("kv_dtype", ctypes.c_int32),
+                ("rope_base", ctypes.c_float), ("page_stride", ctypes.c_int64)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{os.path.basename(LIB_PATH)} not built at {LIB_PATH}; run "
                           "`python -m compressed_attention_cvq_b200.build` (needs nvcc)")
     lib = ctypes.CDLL(LIB_PATH)
     P, I, I64, SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
-    S = ctypes.POINTER(cvq_shape)
+    S, G = ctypes.POINTER(cvq_shape), ctypes.POINTER(cvq_paged)
     sig = {
         "cvq_status_str": (ctypes.c_char_p, [I]),
         "cvq_abi_version": (I, []),
@@ -62,6 +71,14 @@ def _load():
         "cvq_attend": (I, [S, P, I, P, I64, P, P, P, P, I64, I, P, P, P, P]),
         "cvq_fault_status": (I, [ctypes.POINTER(ctypes.c_uint32), I]),
         "cvq_pack_codes6": (I, [S, P, P, P]),
+        "cvq_prefix_workspace_bytes": (SZ, [S, I]),
+        "cvq_prefix_suggest_splits": (I, [S, I, I]),
+        "cvq_prefix_attend": (I, [S, P, I, P, I64, P, P, P, P, I64, I, P, P, I, P, P]),
+        "cvq_paged_append": (I, [G, ctypes.c_int32, P, I64, P, I64, P, I64, I, P, P, P, P, P, P,
+                                 P, P]),
+        "cvq_paged_workspace_bytes": (SZ, [G, I]),
+        "cvq_paged_suggest_splits": (I, [G, I]),
+        "cvq_paged_attend": (I, [G, P, I, P, P, P, P, I, P, P, P, P, I, P, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -89,10 +106,15 @@ EXPORTED = ["cvq_status_str", "cvq_abi_version", "cvq_ptable_bytes", "cvq_partia
             "cvq_decode_attn_gqa", "cvq_combine", "cvq_attend_static",
             "cvq_naive_cache_bytes", "cvq_naive_dequant", "cvq_naive_decode",
             "cvq_encode_append", "cvq_attend_workspace_bytes", "cvq_attend",
-            "cvq_fault_status", "cvq_pack_codes6"]
+            "cvq_fault_status", "cvq_pack_codes6",
+            "cvq_prefix_workspace_bytes", "cvq_prefix_suggest_splits", "cvq_prefix_attend",
+            "cvq_paged_append", "cvq_paged_workspace_bytes", "cvq_paged_suggest_splits",
+            "cvq_paged_attend"]
 CVQ_FAULT_COPY_TIMEOUT = 1
 CVQ_FAULT_BOUNDS = 2
-FAULT_NAMES = {CVQ_FAULT_COPY_TIMEOUT: "copy_timeout", CVQ_FAULT_BOUNDS: "bounds"}
+CVQ_PAGE_FAULT = 4
+FAULT_NAMES = {CVQ_FAULT_COPY_TIMEOUT: "copy_timeout", CVQ_FAULT_BOUNDS: "bounds",
+               CVQ_PAGE_FAULT: "page"}
 
 
 def fault_names(word: int) -> list:

@@ -161,6 +161,11 @@ cvq_status decode_gqa_impl(const cvq_shape* s, const void* q, int q_dtype, const
 
 namespace cvq {
 
+cvq_status check_shape_status(const cvq_shape* s) { return check_shape(s); }
+
+// key and value codebooks have the same size per head in both layouts
+cvq_status check_codebook_stride(const cvq_shape* s, int64_t stride) { return check_stride(stride, key_cb_floats(s)); }
+
 // F_j for every pair, computed in long double
 static void phase_turns_exact(float rope_base, PhaseTurns* out) {
   const long double two_pi = 6.283185307179586476925286766559L;

@@ -1,0 +1,306 @@
+// Decode attention in fp32 on the CUDA cores: a tile of query rows that share a KV head
+// against tiles of 64 cached tokens, one pass with the running maximum and sum of the
+// softmax.  Tokens come from a code cache (decoded and rotated once per tile, then read by
+// every row) or from 16-bit pages.
+//
+// Per tile and CTA: S = Q K^T as 16 x 16 threads of RPT rows x 4 tokens each, operands read
+// from shared memory as float4 along the 128 dims (token rows padded to 132 floats: the 8
+// lanes of a 16-byte phase then start 4 banks apart); the weights go through shared memory
+// transposed so that O += P V reads RPT weights and 8 value dims per thread and token.
+#include "serve.cuh"
+
+namespace cvq {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kTile = 64;          // tokens per tile
+constexpr int kPad = kHeadDim + 4;
+
+// key code and value code lookups of the two layouts
+__device__ __forceinline__ int wide_code(const uint8_t* codes, const ServeArgs& a, int h, int G, int r, int t) {
+  const size_t row = (static_cast<size_t>(h) * kWideGroups + G) * a.R + r;
+  if (a.code_bits == 6) return packed6_code(codes + row * (static_cast<size_t>(a.t_cap) / 4 * 3), t);
+  return codes[row * a.t_cap + t] & 63;
+}
+
+// 8 dims (chunk c) of the key and value of token t of KV head h, decoded from the codes; the
+// key rotated by position t
+__device__ __forceinline__ void decode_chunk(const ServeArgs& a, const unsigned long long* f_tab, int h, int t,
+                                             int c, float (&k)[8], float (&v)[8]) {
+#pragma unroll
+  for (int d = 0; d < 8; ++d) k[d] = v[d] = 0.f;
+  const float* kcb = a.key_cb + h * a.key_cb_stride;
+  const float* vcb = a.val_cb + h * a.val_cb_stride;
+  for (int r = 0; r < a.R; ++r) {
+    size_t ko, vo;
+    if (a.wide) {
+      const int G = c >> 3;
+      const size_t base = (static_cast<size_t>(G) * a.R + r) * kWideCodes;
+      ko = (base + wide_code(a.key_codes, a, h, G, r, t)) * kWideGroupDim + 8 * (c & 7);
+      vo = (base + wide_code(a.val_codes, a, h, G, r, t)) * kWideGroupDim + 8 * (c & 7);
+    } else {
+      const size_t row = ((static_cast<size_t>(h) * a.t_cap + t) * a.R + r) * kGroups + c;
+      const size_t base = (static_cast<size_t>(c) * a.R + r) * kCodes;
+      ko = (base + a.key_codes[row]) * kCodeword;
+      vo = (base + a.val_codes[row]) * kVDims;
+    }
+    const float4 a0 = __ldg(reinterpret_cast<const float4*>(kcb + ko));
+    const float4 a1 = __ldg(reinterpret_cast<const float4*>(kcb + ko) + 1);
+    const float4 b0 = __ldg(reinterpret_cast<const float4*>(vcb + vo));
+    const float4 b1 = __ldg(reinterpret_cast<const float4*>(vcb + vo) + 1);
+    k[0] += a0.x; k[1] += a0.y; k[2] += a0.z; k[3] += a0.w;
+    k[4] += a1.x; k[5] += a1.y; k[6] += a1.z; k[7] += a1.w;
+    v[0] += b0.x; v[1] += b0.y; v[2] += b0.z; v[3] += b0.w;
+    v[4] += b1.x; v[5] += b1.y; v[6] += b1.z; v[7] += b1.w;
+  }
+#pragma unroll
+  for (int p = 0; p < 4; ++p) {
+    const float2 ph = phase_exact(f_tab[4 * c + p] * static_cast<unsigned long long>(static_cast<unsigned>(t)));
+    const float re = k[2 * p], im = k[2 * p + 1];
+    k[2 * p] = re * ph.x - im * ph.y;
+    k[2 * p + 1] = re * ph.y + im * ph.x;
+  }
+}
+
+// 8 dims (chunk c) of token t of sequence b from the pages; false if its page is out of range
+__device__ __forceinline__ bool page_chunk(const ServeArgs& a, int b, int h, int t, int c, float (&k)[8], float (&v)[8]) {
+  const int page = a.page_table[static_cast<size_t>(b) * a.max_pages + (t >> a.page_shift)];
+  if (static_cast<unsigned>(page) >= static_cast<unsigned>(a.n_pages)) {
+    atomicOr(a.fault, kFaultPage);
+    return false;
+  }
+  const size_t at = static_cast<size_t>(page) * a.page_stride +
+                    ((static_cast<size_t>(h) << a.page_shift) + (t & ((1 << a.page_shift) - 1))) * kHeadDim + 8 * c;
+  const uint4 kw = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.k_pages) + at);
+  const uint4 vw = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.v_pages) + at);
+#pragma unroll
+  for (int d = 0; d < 8; ++d) {
+    k[d] = load_any(&kw, a.kv_dtype, d);
+    v[d] = load_any(&vw, a.kv_dtype, d);
+  }
+  return true;
+}
+
+// RB query rows per CTA.  Prefix: rows of one KV head are (sequence, head of the group)
+// pairs, blockIdx.z takes RB of them.  Paged: blockIdx.z is the sequence, its group's heads
+// the rows.
+template <int RB, bool kPaged>
+__global__ void __launch_bounds__(kThreads) attend_f32_kernel(const __grid_constant__ ServeArgs a) {
+  constexpr int RPT = RB / 16;
+  extern __shared__ float4 smem4[];
+  float* sq = reinterpret_cast<float*>(smem4);      // [RB][kPad]
+  float* sk = sq + RB * kPad;                       // [kTile][kPad]
+  float* sv = sk + kTile * kPad;                    // [kTile][128]
+  float* sp = sk;                                   // [kTile][RB], over the keys once they are read
+  __shared__ unsigned long long f_tab[kPairs];
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  const int split = blockIdx.x, h = blockIdx.y;
+  const int rows = kPaged ? a.group : a.batch * a.group;
+  const int r0 = kPaged ? 0 : blockIdx.z * RB;
+  const int b0 = kPaged ? blockIdx.z : 0;
+  int L = a.lens[b0];
+  L = L < 0 ? 0 : (L > a.t_cap ? a.t_cap : L);
+  const int start = static_cast<int>(min(static_cast<long long>(split) * a.split_tokens, static_cast<long long>(L)));
+  const int end = static_cast<int>(min(static_cast<long long>(start) + a.split_tokens, static_cast<long long>(L)));
+  // global row (sequence, query head) of local row r
+  auto grow = [&](int r) {
+    const int rr = r0 + r;
+    const int b = kPaged ? b0 : rr / a.group, hh = kPaged ? rr : rr % a.group;
+    return static_cast<size_t>(b) * a.n_q_heads + h * a.group + hh;
+  };
+  for (int i = tid; i < kPairs; i += kThreads) f_tab[i] = a.phase.F[i];
+  for (int i = tid; i < RB * kHeadDim; i += kThreads) {
+    const int r = i / kHeadDim, d = i % kHeadDim;
+    float x = 0.f;
+    if (r0 + r < rows && start < end) x = load_any(a.q, a.q_dtype, grow(r) * kHeadDim + d);
+    sq[r * kPad + d] = x * (0.08838834764831845f * kLog2e);
+  }
+  float m[RPT], l[RPT], o[RPT][8];
+#pragma unroll
+  for (int i = 0; i < RPT; ++i) {
+    m[i] = -INFINITY;
+    l[i] = 0.f;
+#pragma unroll
+    for (int d = 0; d < 8; ++d) o[i][d] = 0.f;
+  }
+  for (int t0 = start; t0 < end; t0 += kTile) {
+    __syncthreads();                                // the last tile's readers are done
+#pragma unroll
+    for (int u = 0; u < kTile * 16 / kThreads; ++u) {
+      const int i = tid + u * kThreads, tk = i >> 4, c = i & 15, t = t0 + tk;
+      float k[8], v[8];
+      bool have = t < end;
+      if (have) {
+        if constexpr (kPaged) have = page_chunk(a, b0, h, t, c, k, v);
+        else decode_chunk(a, f_tab, h, t, c, k, v);
+      }
+      if (!have) {
+#pragma unroll
+        for (int d = 0; d < 8; ++d) k[d] = v[d] = 0.f;
+      }
+      float4* kd = reinterpret_cast<float4*>(sk + tk * kPad + 8 * c);
+      kd[0] = make_float4(k[0], k[1], k[2], k[3]);
+      kd[1] = make_float4(k[4], k[5], k[6], k[7]);
+      float4* vd = reinterpret_cast<float4*>(sv + tk * kHeadDim + 8 * c);
+      vd[0] = make_float4(v[0], v[1], v[2], v[3]);
+      vd[1] = make_float4(v[4], v[5], v[6], v[7]);
+    }
+    __syncthreads();
+    float s[RPT][4];
+#pragma unroll
+    for (int i = 0; i < RPT; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+    for (int d = 0; d < kHeadDim; d += 4) {
+      float4 qv[RPT], kv[4];
+#pragma unroll
+      for (int i = 0; i < RPT; ++i) qv[i] = *reinterpret_cast<const float4*>(sq + (ty * RPT + i) * kPad + d);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) kv[j] = *reinterpret_cast<const float4*>(sk + (tx + 16 * j) * kPad + d);
+#pragma unroll
+      for (int i = 0; i < RPT; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          s[i][j] = fmaf(qv[i].x, kv[j].x, s[i][j]);
+          s[i][j] = fmaf(qv[i].y, kv[j].y, s[i][j]);
+          s[i][j] = fmaf(qv[i].z, kv[j].z, s[i][j]);
+          s[i][j] = fmaf(qv[i].w, kv[j].w, s[i][j]);
+        }
+    }
+    __syncthreads();                                // sp takes the place of sk
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int t = t0 + tx + 16 * j;
+      bool seen = t < end;
+      if constexpr (kPaged) {
+        if (seen)
+          seen = static_cast<unsigned>(a.page_table[static_cast<size_t>(b0) * a.max_pages + (t >> a.page_shift)]) <
+                 static_cast<unsigned>(a.n_pages);
+      }
+      if (!seen) {
+#pragma unroll
+        for (int i = 0; i < RPT; ++i) s[i][j] = -INFINITY;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < RPT; ++i) {
+      float mx = fmaxf(fmaxf(s[i][0], s[i][1]), fmaxf(s[i][2], s[i][3]));
+#pragma unroll
+      for (int w = 8; w > 0; w >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
+      const float mn = fmaxf(m[i], mx);
+      const float ref = mn == -INFINITY ? 0.f : mn;          // nothing seen yet: every weight 0
+      const float alpha = exp2f(m[i] - ref);
+      m[i] = mn;
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float p = exp2f(s[i][j] - ref);
+        sum += p;
+        sp[(tx + 16 * j) * RB + ty * RPT + i] = p;
+      }
+      l[i] = fmaf(l[i], alpha, sum);
+#pragma unroll
+      for (int d = 0; d < 8; ++d) o[i][d] *= alpha;
+    }
+    __syncthreads();
+    for (int t = 0; t < kTile; ++t) {
+      float p[RPT];
+      if constexpr (RPT == 4) {
+        const float4 pv = *reinterpret_cast<const float4*>(sp + t * RB + ty * RPT);
+        p[0] = pv.x; p[1] = pv.y; p[2] = pv.z; p[3] = pv.w;
+      } else {
+#pragma unroll
+        for (int i = 0; i < RPT; ++i) p[i] = sp[t * RB + ty * RPT + i];
+      }
+      const float4 v0 = *reinterpret_cast<const float4*>(sv + t * kHeadDim + 4 * tx);
+      const float4 v1 = *reinterpret_cast<const float4*>(sv + t * kHeadDim + 64 + 4 * tx);
+#pragma unroll
+      for (int i = 0; i < RPT; ++i) {
+        o[i][0] = fmaf(p[i], v0.x, o[i][0]);
+        o[i][1] = fmaf(p[i], v0.y, o[i][1]);
+        o[i][2] = fmaf(p[i], v0.z, o[i][2]);
+        o[i][3] = fmaf(p[i], v0.w, o[i][3]);
+        o[i][4] = fmaf(p[i], v1.x, o[i][4]);
+        o[i][5] = fmaf(p[i], v1.y, o[i][5]);
+        o[i][6] = fmaf(p[i], v1.z, o[i][6]);
+        o[i][7] = fmaf(p[i], v1.w, o[i][7]);
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < RPT; ++i) {
+#pragma unroll
+    for (int w = 8; w > 0; w >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], w);
+    const int r = ty * RPT + i;
+    if (r0 + r >= rows) continue;
+    const size_t at = grow(r) * a.n_splits + split;
+    if (tx == 0) {
+      a.part_m[at] = m[i];
+      a.part_l[at] = l[i];
+    }
+    if (start >= end) continue;
+    float4* po = reinterpret_cast<float4*>(a.part_o + at * kHeadDim);
+    po[tx] = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
+    po[16 + tx] = make_float4(o[i][4], o[i][5], o[i][6], o[i][7]);
+  }
+}
+
+// Merge of split partial states (m in log2 units), with an earlier state if there is one:
+// one CTA per (sequence, query head), one thread per output dim.
+__global__ void __launch_bounds__(kHeadDim) merge_kernel(const __grid_constant__ ServeArgs a) {
+  const size_t row = blockIdx.x;
+  const int d = threadIdx.x;
+  const float* pm = a.part_m + row * a.n_splits;
+  const float* pl = a.part_l + row * a.n_splits;
+  const float* po = a.part_o + row * a.n_splits * kHeadDim;
+  const float pz = a.prev_lse != nullptr ? a.prev_lse[row] * kLog2e : -INFINITY;
+  float M = pz;
+  for (int s = 0; s < a.n_splits; ++s) M = fmaxf(M, pm[s]);
+  const float ref = M == -INFINITY ? 0.f : M;
+  float L = 0.f, acc = 0.f;
+  if (pz != -INFINITY) {
+    L = exp2f(pz - ref);
+    acc = L * a.prev_out[row * kHeadDim + d];
+  }
+  for (int s = 0; s < a.n_splits; ++s) {
+    if (pm[s] == -INFINITY && !(pl[s] != 0.f)) continue;      // a split with no token has no o
+    const float f = exp2f(pm[s] - ref);
+    L = fmaf(pl[s], f, L);
+    acc = fmaf(po[static_cast<size_t>(s) * kHeadDim + d], f, acc);
+  }
+  __syncthreads();                                            // prev_lse may be lse
+  store_any(a.out, a.out_dtype, row * kHeadDim + d, L == 0.f ? 0.f : acc / L);
+  if (d == 0) a.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+}
+
+template <int RB, bool kPaged>
+cudaError_t run(const ServeArgs& a, dim3 grid, cudaStream_t stream) {
+  static PerDeviceFlag flag;
+  const size_t bytes = (static_cast<size_t>(RB) * kPad + kTile * kPad + kTile * kHeadDim) * sizeof(float);
+  static_assert(RB <= kPad, "the weights fit over the keys");
+  const cudaError_t e = set_smem_limit_once(flag, attend_f32_kernel<RB, kPaged>, bytes);
+  if (e != cudaSuccess) return e;
+  attend_f32_kernel<RB, kPaged><<<grid, kThreads, bytes, stream>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_prefix_f32(const ServeArgs& a, cudaStream_t stream) {
+  const int rows = a.batch * a.group;
+  const dim3 grid(a.n_splits, a.n_kv_heads, rows <= 16 ? 1 : (rows + 63) / 64);
+  return rows <= 16 ? run<16, false>(a, grid, stream) : run<64, false>(a, grid, stream);
+}
+
+cudaError_t launch_paged_attend(const ServeArgs& a, cudaStream_t stream) {
+  const cudaError_t e = run<16, true>(a, dim3(a.n_splits, a.n_kv_heads, a.batch), stream);
+  return e != cudaSuccess ? e : launch_merge(a, stream);
+}
+
+cudaError_t launch_merge(const ServeArgs& a, cudaStream_t stream) {
+  merge_kernel<<<static_cast<unsigned>(a.batch) * a.n_q_heads, kHeadDim, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace cvq

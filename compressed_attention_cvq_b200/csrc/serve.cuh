@@ -1,0 +1,98 @@
+// Shared definitions of the serving operators: shared-prefix attention, the paged 16-bit
+// cache and the attention over it.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+
+namespace cvq {
+
+constexpr unsigned int kFaultPage = CVQ_PAGE_FAULT;
+
+// Arguments of the attention kernels.  Split partial states are [B, Hq, n_splits] rows as in
+// the other decode kernels, with m in log2 units (the kernels work with exp2); a split with
+// no token stores m = -inf and l = 0 and leaves its o unwritten.
+struct ServeArgs {
+  const void* q;
+  int q_dtype;
+  int batch, n_q_heads, n_kv_heads, group;
+  int n_splits, split_tokens;
+  float* part_o;
+  float* part_m;
+  float* part_l;
+  int* counters;
+  const int32_t* lens;            // prefix_len [1] or seq_lens [B]
+  int t_cap;                      // tokens the cache (or a table row) can hold
+  unsigned int* fault;
+  const float* prev_out;
+  const float* prev_lse;
+  void* out;
+  int out_dtype;
+  float* lse;
+  // code cache (prefix)
+  const float* key_cb;
+  const float* val_cb;
+  long long key_cb_stride, val_cb_stride;
+  const uint8_t* key_codes;
+  const uint8_t* val_codes;
+  int R, wide, code_bits;
+  PhaseTurns phase;
+  // paged cache
+  const void* k_pages;
+  const void* v_pages;
+  const int32_t* page_table;
+  int kv_dtype, page_shift, n_pages, max_pages;
+  long long page_stride;
+};
+
+struct AppendArgs {
+  const void* q;
+  const void* k;
+  const void* v;
+  long long q_stride, k_stride, v_stride;
+  const int32_t* tok_offsets;
+  const int32_t* seq_lens;
+  const int32_t* pos_offsets;
+  const int32_t* page_table;
+  void* k_pages;
+  void* v_pages;
+  void* q_out;
+  int n_tokens, batch, n_q_heads, n_kv_heads, page_shift, n_pages, max_pages;
+  long long page_stride;
+  unsigned int* fault;
+  PhaseTurns phase;
+};
+
+__device__ __forceinline__ float load_any(const void* p, int dtype, size_t i) {
+  if (dtype == CVQ_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+  if (dtype == CVQ_F16) return __half2float(static_cast<const __half*>(p)[i]);
+  return static_cast<const float*>(p)[i];
+}
+__device__ __forceinline__ void store_any(void* p, int dtype, size_t i, float x) {
+  if (dtype == CVQ_BF16) static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(x);
+  else if (dtype == CVQ_F16) static_cast<__half*>(p)[i] = __float2half_rn(x);
+  else static_cast<float*>(p)[i] = x;
+}
+
+// e^{2 pi i turn64 / 2^64} to full fp32 accuracy (phase_from_turn's __sincosf is good to
+// 2^-21; here outputs may be fp32): the signed top 32 bits are the angle in units of
+// 2^-31 pi, rounded once to fp32.
+__device__ __forceinline__ float2 phase_exact(unsigned long long turn64) {
+  const float x = static_cast<float>(static_cast<int>(turn64 >> 32)) * 4.656612873077393e-10f;
+  float s, c;
+  sincospif(x, &s, &c);
+  return make_float2(c, s);
+}
+
+// the checks of cvq_shape and of a codebook head stride (api.cu)
+cvq_status check_shape_status(const cvq_shape* s);
+cvq_status check_codebook_stride(const cvq_shape* s, int64_t stride);
+
+cudaError_t launch_prefix_f32(const ServeArgs& a, cudaStream_t stream);
+cudaError_t launch_paged_attend(const ServeArgs& a, cudaStream_t stream);
+cudaError_t launch_merge(const ServeArgs& a, cudaStream_t stream);
+cudaError_t launch_paged_append(const AppendArgs& a, int in_dtype, int kv_dtype, cudaStream_t stream);
+
+}  // namespace cvq

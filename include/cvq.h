@@ -66,7 +66,7 @@ extern "C" {
 #define CVQ_API
 #endif
 
-#define CVQ_ABI_VERSION 3
+#define CVQ_ABI_VERSION 4
 #define CVQ_HEAD_DIM 128
 #define CVQ_GROUPS 16
 #define CVQ_CODES 256
@@ -82,7 +82,8 @@ typedef enum {
   CVQ_ERR_STATIC_LIMIT = 7 /* cvq_attend_static: partials exceed the static scratch  */
 } cvq_status;
 
-typedef enum { CVQ_F32 = 0, CVQ_BF16 = 1 } cvq_dtype;
+/* CVQ_F16 is accepted by the shared-prefix and paged calls only. */
+typedef enum { CVQ_F32 = 0, CVQ_BF16 = 1, CVQ_F16 = 2 } cvq_dtype;
 
 typedef struct {
   int32_t batch;      /* 1 <= B <= 65535                                      */
@@ -345,6 +346,128 @@ CVQ_API cvq_status cvq_attend_static(const cvq_shape* shape, const void* q, int 
                                      float* lse, void* stream);
 
 /* ---------------------------------------------------------------------------------
+ * cvq_prefix_attend -- one decode step of a whole batch against ONE compressed prefix
+ * that every sequence shares (a system prompt, a document), computed once for all: each
+ * cached token is decoded once per KV head and read by the query heads of every sequence.
+ *   For sequence b and query head hq, with h = hq / (Hq / Hkv), the formulas of the top of
+ *   this file over the tokens t = 0..L-1 of the one cache, L = prefix_len[0].  Fold the
+ *   state of each sequence's own tokens in with cvq_paged_attend.
+ *
+ *   shape      batch is the number of sequences; t_cap the capacity of the one cache.
+ *              Both layouts (group_dim 8 with R = 1 or 2, group_dim 64 with R = 1..22 and
+ *              either code_bits), every supported Hq / Hkv (1, 2, 4, 8)
+ *   q          [B, Hq, 128] fp32, bf16 or fp16, already rotated
+ *   key_cb, val_cb and their head strides as in cvq_decode_attn_gqa
+ *   key_codes, val_codes  the cache of one sequence: [Hkv, t_cap, R, 16], or planar
+ *              [Hkv, 2, R, t_cap] (packed [Hkv, 2, R, 3 t_cap / 4])
+ *   prefix_len [1] int32 (device), clamped to [0, t_cap]; 0: out = 0, lse = -inf
+ *   workspace  cvq_prefix_workspace_bytes(shape, n_splits) bytes, 16-byte aligned; its
+ *              contents before and after a call are of no meaning.  Calls that share a
+ *              workspace must be ordered on one stream
+ *   out        [B, Hq, 128] of out_dtype (fp32, bf16 or fp16), 16-byte aligned
+ *   lse        [B, Hq] fp32, natural log
+ *   Arithmetic: fp32 queries are multiplied in fp32.
+ *   Errors as in cvq_attend.
+ * ------------------------------------------------------------------------------- */
+CVQ_API size_t cvq_prefix_workspace_bytes(const cvq_shape* shape, int n_splits);
+/* A split count for this shape and query type on `sm_count` SMs (a suggestion). */
+CVQ_API int cvq_prefix_suggest_splits(const cvq_shape* shape, int q_dtype, int sm_count);
+CVQ_API cvq_status cvq_prefix_attend(const cvq_shape* shape, const void* q, int q_dtype,
+                                     const float* key_cb, int64_t key_cb_head_stride,
+                                     const uint8_t* key_codes, const uint8_t* val_codes,
+                                     const int32_t* prefix_len, const float* val_cb,
+                                     int64_t val_cb_head_stride, int n_splits, void* workspace,
+                                     void* out, int out_dtype, float* lse, void* stream);
+
+/* ---------------------------------------------------------------------------------
+ * A 16-bit paged cache for tokens that are not (or not yet) encoded: what each sequence
+ * generates behind a compressed prefix, or its most recent window.  Keys are stored
+ * rotated.  A pool holds n_pages pages [Hkv, page_size, 128] of kv_dtype, page_stride
+ * elements apart (0 = dense, Hkv * page_size * 128); keys and values have a pool each (or
+ * one array with the two interleaved, at two base addresses and one page_stride).  Token p
+ * of sequence b is row p % page_size of page page_table[b][p / page_size].
+ * ------------------------------------------------------------------------------- */
+typedef struct {
+  int32_t batch;       /* 1 <= B <= 65535                                       */
+  int32_t n_q_heads;   /* 1 <= Hq <= 65535, a multiple of n_kv_heads           */
+  int32_t n_kv_heads;  /* Hkv >= 1; Hq/Hkv in {1, 2, 4, 8}                      */
+  int32_t head_dim;    /* must be 128                                           */
+  int32_t page_size;   /* tokens per page: a power of two, 1..1024              */
+  int32_t n_pages;     /* pages in each pool, >= 1                              */
+  int32_t max_pages;   /* row length of the page table, >= 1;
+                          max_pages * page_size < 2^31                          */
+  int32_t kv_dtype;    /* CVQ_BF16 or CVQ_F16                                   */
+  float rope_base;     /* RoPE base, > 1                                        */
+  int64_t page_stride; /* elements between pages: 0, or a multiple of 8 that is
+                          >= n_kv_heads * page_size * 128                       */
+} cvq_paged;
+
+/* ---------------------------------------------------------------------------------
+ * cvq_paged_append -- write the keys and values of new tokens into the pages, keys
+ * rotated on the way, and rotate the tokens' queries.
+ *   Token i with tok_offsets[b] <= i < tok_offsets[b+1] belongs to sequence b.  seq_lens[b]
+ *   is the sequence's length AFTER the append (the array that cvq_paged_attend then takes),
+ *   so the token's index in the sequence is
+ *     p = seq_lens[b] - (tok_offsets[b+1] - i),
+ *   and its RoPE position pos_offsets[b] + p (pos_offsets: the length of the prefix that
+ *   the sequence continues; NULL = 0).  Angles are reduced exactly at any position.
+ *
+ *   k, v       [n_tokens, Hkv, 128] of in_dtype (fp32, bf16, fp16): heads dense, tokens
+ *              k_stride / v_stride elements apart (views of a fused projection); 16-byte
+ *              aligned, strides a multiple of 16 bytes and >= Hkv * 128
+ *   q, q_out   [n_tokens, Hq, 128] of in_dtype, tokens q_stride elements apart; q_out is
+ *              dense and may be q itself when q is dense.  Both NULL: no queries
+ *   tok_offsets [B+1], seq_lens [B], pos_offsets [B] or NULL, page_table [B, max_pages]:
+ *              int32 (device); tok_offsets does not decrease and starts at 0.  Tokens
+ *              from tok_offsets[B] on (padding) are left alone: nothing is written for
+ *              them, in the pages or in q_out
+ *   A token whose index p falls outside [0, max_pages * page_size) or whose page is outside
+ *   [0, n_pages) is not stored, and CVQ_PAGE_FAULT is set in the fault word; its query is
+ *   rotated all the same.  No two tokens may be sent to one row (a page held by two
+ *   sequences): which of them the row then holds is not defined.
+ *   Errors: CVQ_ERR_NULL / CVQ_ERR_ALIGN / CVQ_ERR_SHAPE / CVQ_ERR_UNSUPPORTED before any
+ *   launch; n_tokens = 0 is CVQ_OK.  Asynchronous on `stream`.
+ * ------------------------------------------------------------------------------- */
+CVQ_API cvq_status cvq_paged_append(const cvq_paged* paged, int32_t n_tokens, const void* q,
+                                    int64_t q_stride, const void* k, int64_t k_stride,
+                                    const void* v, int64_t v_stride, int in_dtype,
+                                    const int32_t* tok_offsets, const int32_t* seq_lens,
+                                    const int32_t* pos_offsets, const int32_t* page_table,
+                                    void* k_pages, void* v_pages, void* q_out, void* stream);
+
+/* ---------------------------------------------------------------------------------
+ * cvq_paged_attend -- decode attention of one query token per sequence over its pages,
+ * and the merge with the state of an earlier part of the sequence.
+ *   s_p = q . k_p / sqrt(128), p = 0..seq_lens[b]-1 (clamped to [0, max_pages * page_size]);
+ *   (o, z) = (softmax(s) v, ln sum exp s).  Without prev_*: out = o, lse = z.  With them:
+ *   lse = ln(e^z + e^prev_lse), out = e^(z - lse) o + e^(prev_lse - lse) prev_out: the
+ *   attention over both parts, as from cvq_prefix_attend or cvq_attend over the part before.
+ *   An empty sequence gives out = 0 and lse = -inf, or the earlier state; prev_out is not
+ *   used where prev_lse = -inf.
+ *
+ *   q          [B, Hq, 128] fp32, bf16 or fp16, rotated (q_out of cvq_paged_append)
+ *   prev_out   [B, Hq, 128] fp32, prev_lse [B, Hq] fp32, both or neither NULL; they may be
+ *              out (when fp32) and lse themselves
+ *   workspace  cvq_paged_workspace_bytes(paged, n_splits) bytes, 16-byte aligned, with the
+ *              rules of cvq_attend's: zero when the first call starts; a call leaves what
+ *              the next call of the same shape and n_splits needs; calls that share one are
+ *              ordered on one stream
+ *   out, lse   as in cvq_prefix_attend
+ *   A page index outside [0, n_pages) is not followed: its tokens count as absent, and
+ *   CVQ_PAGE_FAULT is set in the fault word.  Rows behind seq_lens[b] are not read, whatever
+ *   they hold.  Products are exact and sums are kept in fp32, whatever the types.
+ * ------------------------------------------------------------------------------- */
+CVQ_API size_t cvq_paged_workspace_bytes(const cvq_paged* paged, int n_splits);
+/* A split count for sequences of up to max_pages * page_size tokens (a suggestion). */
+CVQ_API int cvq_paged_suggest_splits(const cvq_paged* paged, int sm_count);
+CVQ_API cvq_status cvq_paged_attend(const cvq_paged* paged, const void* q, int q_dtype,
+                                    const void* k_pages, const void* v_pages,
+                                    const int32_t* page_table, const int32_t* seq_lens,
+                                    int n_splits, void* workspace, const float* prev_out,
+                                    const float* prev_lse, void* out, int out_dtype, float* lse,
+                                    void* stream);
+
+/* ---------------------------------------------------------------------------------
  * cvq_fault_status -- the device fault word of the current device.  The decode kernels
  * that stage codebooks with the TMA engine (cvq_decode_attn_gqa / cvq_attend /
  * cvq_attend_static with 4 query heads per KV head, and every g = 64 decode) wait for
@@ -358,6 +481,8 @@ CVQ_API cvq_status cvq_attend_static(const cvq_shape* shape, const void* q, int 
  *         between the CTAs of a pair, and the partial-state rows and arrival counter of
  *         every work unit.  A failed check skips its access (a skipped load reads 0) and
  *         the kernel runs on; the outputs of that call are then invalid.
+ *         CVQ_PAGE_FAULT = a page-table entry or a token index of a paged call was out of
+ *         range; the access was skipped.
  *   flags (host): receives the word.  clear != 0 resets it to 0 afterwards.
  *   Synchronous: waits for the device (cudaMemcpy).  The first call on a device looks up
  *   the word's address (cudaGetSymbolAddress), as the first decode call does; make that
@@ -366,6 +491,7 @@ CVQ_API cvq_status cvq_attend_static(const cvq_shape* shape, const void* q, int 
  * ------------------------------------------------------------------------------- */
 #define CVQ_FAULT_COPY_TIMEOUT 1u
 #define CVQ_FAULT_BOUNDS 2u
+#define CVQ_PAGE_FAULT 4u
 CVQ_API cvq_status cvq_fault_status(uint32_t* flags, int clear);
 
 #ifdef __cplusplus
