@@ -1,7 +1,6 @@
-// Decode attention in fp32 on the CUDA cores: a tile of query rows that share a KV head
-// against tiles of 64 cached tokens, one pass with the running maximum and sum of the
-// softmax.  Tokens come from a code cache (decoded and rotated once per tile, then read by
-// every row) or from 16-bit pages.
+// Shared-prefix attention in fp32 on the CUDA cores: a tile of query rows that share a KV
+// head against tiles of 64 cached tokens, one pass with the running maximum and sum of the
+// softmax.  A tile is decoded from its codes and rotated once, then read by every row.
 //
 // Per tile and CTA: S = Q K^T as 16 x 16 threads of RPT rows x 4 tokens each, operands read
 // from shared memory as float4 along the 128 dims (token rows padded to 132 floats: the 8
@@ -63,29 +62,9 @@ __device__ __forceinline__ void decode_chunk(const ServeArgs& a, const unsigned 
   }
 }
 
-// 8 dims (chunk c) of token t of sequence b from the pages; false if its page is out of range
-__device__ __forceinline__ bool page_chunk(const ServeArgs& a, int b, int h, int t, int c, float (&k)[8], float (&v)[8]) {
-  const int page = a.page_table[static_cast<size_t>(b) * a.max_pages + (t >> a.page_shift)];
-  if (static_cast<unsigned>(page) >= static_cast<unsigned>(a.n_pages)) {
-    atomicOr(a.fault, kFaultPage);
-    return false;
-  }
-  const size_t at = static_cast<size_t>(page) * a.page_stride +
-                    ((static_cast<size_t>(h) << a.page_shift) + (t & ((1 << a.page_shift) - 1))) * kHeadDim + 8 * c;
-  const uint4 kw = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.k_pages) + at);
-  const uint4 vw = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.v_pages) + at);
-#pragma unroll
-  for (int d = 0; d < 8; ++d) {
-    k[d] = load_any(&kw, a.kv_dtype, d);
-    v[d] = load_any(&vw, a.kv_dtype, d);
-  }
-  return true;
-}
-
-// RB query rows per CTA.  Prefix: rows of one KV head are (sequence, head of the group)
-// pairs, blockIdx.z takes RB of them.  Paged: blockIdx.z is the sequence, its group's heads
-// the rows.
-template <int RB, bool kPaged>
+// RB query rows per CTA: the rows of a KV head are (sequence, head of the group) pairs, and
+// blockIdx.z takes RB of them.
+template <int RB>
 __global__ void __launch_bounds__(kThreads) attend_f32_kernel(const __grid_constant__ ServeArgs a) {
   constexpr int RPT = RB / 16;
   extern __shared__ float4 smem4[];
@@ -96,18 +75,16 @@ __global__ void __launch_bounds__(kThreads) attend_f32_kernel(const __grid_const
   __shared__ unsigned long long f_tab[kPairs];
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   const int split = blockIdx.x, h = blockIdx.y;
-  const int rows = kPaged ? a.group : a.batch * a.group;
-  const int r0 = kPaged ? 0 : blockIdx.z * RB;
-  const int b0 = kPaged ? blockIdx.z : 0;
-  int L = a.lens[b0];
+  const int rows = a.batch * a.group;
+  const int r0 = blockIdx.z * RB;
+  int L = a.lens[0];
   L = L < 0 ? 0 : (L > a.t_cap ? a.t_cap : L);
   const int start = static_cast<int>(min(static_cast<long long>(split) * a.split_tokens, static_cast<long long>(L)));
   const int end = static_cast<int>(min(static_cast<long long>(start) + a.split_tokens, static_cast<long long>(L)));
   // global row (sequence, query head) of local row r
   auto grow = [&](int r) {
     const int rr = r0 + r;
-    const int b = kPaged ? b0 : rr / a.group, hh = kPaged ? rr : rr % a.group;
-    return static_cast<size_t>(b) * a.n_q_heads + h * a.group + hh;
+    return static_cast<size_t>(rr / a.group) * a.n_q_heads + h * a.group + rr % a.group;
   };
   for (int i = tid; i < kPairs; i += kThreads) f_tab[i] = a.phase.F[i];
   for (int i = tid; i < RB * kHeadDim; i += kThreads) {
@@ -130,12 +107,9 @@ __global__ void __launch_bounds__(kThreads) attend_f32_kernel(const __grid_const
     for (int u = 0; u < kTile * 16 / kThreads; ++u) {
       const int i = tid + u * kThreads, tk = i >> 4, c = i & 15, t = t0 + tk;
       float k[8], v[8];
-      bool have = t < end;
-      if (have) {
-        if constexpr (kPaged) have = page_chunk(a, b0, h, t, c, k, v);
-        else decode_chunk(a, f_tab, h, t, c, k, v);
-      }
-      if (!have) {
+      if (t < end) {
+        decode_chunk(a, f_tab, h, t, c, k, v);
+      } else {
 #pragma unroll
         for (int d = 0; d < 8; ++d) k[d] = v[d] = 0.f;
       }
@@ -171,14 +145,7 @@ __global__ void __launch_bounds__(kThreads) attend_f32_kernel(const __grid_const
     __syncthreads();                                // sp takes the place of sk
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int t = t0 + tx + 16 * j;
-      bool seen = t < end;
-      if constexpr (kPaged) {
-        if (seen)
-          seen = static_cast<unsigned>(a.page_table[static_cast<size_t>(b0) * a.max_pages + (t >> a.page_shift)]) <
-                 static_cast<unsigned>(a.n_pages);
-      }
-      if (!seen) {
+      if (t0 + tx + 16 * j >= end) {
 #pragma unroll
         for (int i = 0; i < RPT; ++i) s[i][j] = -INFINITY;
       }
@@ -246,42 +213,36 @@ __global__ void __launch_bounds__(kThreads) attend_f32_kernel(const __grid_const
   }
 }
 
-// Merge of split partial states (m in log2 units), with an earlier state if there is one:
-// one CTA per (sequence, query head), one thread per output dim.
+// Merge of split partial states (m in log2 units): one CTA per (sequence, query head), one
+// thread per output dim.
 __global__ void __launch_bounds__(kHeadDim) merge_kernel(const __grid_constant__ ServeArgs a) {
   const size_t row = blockIdx.x;
   const int d = threadIdx.x;
   const float* pm = a.part_m + row * a.n_splits;
   const float* pl = a.part_l + row * a.n_splits;
   const float* po = a.part_o + row * a.n_splits * kHeadDim;
-  const float pz = a.prev_lse != nullptr ? a.prev_lse[row] * kLog2e : -INFINITY;
-  float M = pz;
+  float M = -INFINITY;
   for (int s = 0; s < a.n_splits; ++s) M = fmaxf(M, pm[s]);
   const float ref = M == -INFINITY ? 0.f : M;
   float L = 0.f, acc = 0.f;
-  if (pz != -INFINITY) {
-    L = exp2f(pz - ref);
-    acc = L * a.prev_out[row * kHeadDim + d];
-  }
   for (int s = 0; s < a.n_splits; ++s) {
     if (pm[s] == -INFINITY && !(pl[s] != 0.f)) continue;      // a split with no token has no o
     const float f = exp2f(pm[s] - ref);
     L = fmaf(pl[s], f, L);
     acc = fmaf(po[static_cast<size_t>(s) * kHeadDim + d], f, acc);
   }
-  __syncthreads();                                            // prev_lse may be lse
   store_any(a.out, a.out_dtype, row * kHeadDim + d, L == 0.f ? 0.f : acc / L);
   if (d == 0) a.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
 }
 
-template <int RB, bool kPaged>
+template <int RB>
 cudaError_t run(const ServeArgs& a, dim3 grid, cudaStream_t stream) {
   static PerDeviceFlag flag;
   const size_t bytes = (static_cast<size_t>(RB) * kPad + kTile * kPad + kTile * kHeadDim) * sizeof(float);
   static_assert(RB <= kPad, "the weights fit over the keys");
-  const cudaError_t e = set_smem_limit_once(flag, attend_f32_kernel<RB, kPaged>, bytes);
+  const cudaError_t e = set_smem_limit_once(flag, attend_f32_kernel<RB>, bytes);
   if (e != cudaSuccess) return e;
-  attend_f32_kernel<RB, kPaged><<<grid, kThreads, bytes, stream>>>(a);
+  attend_f32_kernel<RB><<<grid, kThreads, bytes, stream>>>(a);
   return cudaGetLastError();
 }
 
@@ -290,12 +251,7 @@ cudaError_t run(const ServeArgs& a, dim3 grid, cudaStream_t stream) {
 cudaError_t launch_prefix_f32(const ServeArgs& a, cudaStream_t stream) {
   const int rows = a.batch * a.group;
   const dim3 grid(a.n_splits, a.n_kv_heads, rows <= 16 ? 1 : (rows + 63) / 64);
-  return rows <= 16 ? run<16, false>(a, grid, stream) : run<64, false>(a, grid, stream);
-}
-
-cudaError_t launch_paged_attend(const ServeArgs& a, cudaStream_t stream) {
-  const cudaError_t e = run<16, true>(a, dim3(a.n_splits, a.n_kv_heads, a.batch), stream);
-  return e != cudaSuccess ? e : launch_merge(a, stream);
+  return rows <= 16 ? run<16>(a, grid, stream) : run<64>(a, grid, stream);
 }
 
 cudaError_t launch_merge(const ServeArgs& a, cudaStream_t stream) {
