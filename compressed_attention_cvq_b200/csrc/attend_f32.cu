@@ -79,8 +79,9 @@ __global__ void __launch_bounds__(kThreads) attend_f32_kernel(const __grid_const
   const int r0 = blockIdx.z * RB;
   int L = a.lens[0];
   L = L < 0 ? 0 : (L > a.t_cap ? a.t_cap : L);
-  const int start = static_cast<int>(min(static_cast<long long>(split) * a.split_tokens, static_cast<long long>(L)));
-  const int end = static_cast<int>(min(static_cast<long long>(start) + a.split_tokens, static_cast<long long>(L)));
+  const long long per = ((L + a.n_splits - 1LL) / a.n_splits + kTile - 1) / kTile * kTile;
+  const int start = static_cast<int>(min(per * split, static_cast<long long>(L)));
+  const int end = static_cast<int>(min(start + per, static_cast<long long>(L)));
   // global row (sequence, query head) of local row r
   auto grow = [&](int r) {
     const int rr = r0 + r;
@@ -201,7 +202,7 @@ __global__ void __launch_bounds__(kThreads) attend_f32_kernel(const __grid_const
     for (int w = 8; w > 0; w >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], w);
     const int r = ty * RPT + i;
     if (r0 + r >= rows) continue;
-    const size_t at = grow(r) * a.n_splits + split;
+    const size_t at = grow(r) * a.n_parts + split;
     if (tx == 0) {
       a.part_m[at] = m[i];
       a.part_l[at] = l[i];
@@ -213,26 +214,47 @@ __global__ void __launch_bounds__(kThreads) attend_f32_kernel(const __grid_const
   }
 }
 
-// Merge of split partial states (m in log2 units): one CTA per (sequence, query head), one
-// thread per output dim.
-__global__ void __launch_bounds__(kHeadDim) merge_kernel(const __grid_constant__ ServeArgs a) {
-  const size_t row = blockIdx.x;
-  const int d = threadIdx.x;
-  const float* pm = a.part_m + row * a.n_splits;
-  const float* pl = a.part_l + row * a.n_splits;
-  const float* po = a.part_o + row * a.n_splits * kHeadDim;
-  float M = -INFINITY;
-  for (int s = 0; s < a.n_splits; ++s) M = fmaxf(M, pm[s]);
-  const float ref = M == -INFINITY ? 0.f : M;
-  float L = 0.f, acc = 0.f;
-  for (int s = 0; s < a.n_splits; ++s) {
-    if (pm[s] == -INFINITY && !(pl[s] != 0.f)) continue;      // a split with no token has no o
-    const float f = exp2f(pm[s] - ref);
-    L = fmaf(pl[s], f, L);
-    acc = fmaf(po[static_cast<size_t>(s) * kHeadDim + d], f, acc);
+// Merge of the partial states of a row (m in log2 units): one warp per (sequence, query head),
+// 4 dims a lane, U states in flight.
+constexpr int kMergeWarps = 4;
+__global__ void __launch_bounds__(32 * kMergeWarps) merge_kernel(const __grid_constant__ ServeArgs a) {
+  const size_t row = static_cast<size_t>(blockIdx.x) * kMergeWarps + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (row >= static_cast<size_t>(a.batch) * a.n_q_heads) return;
+  const float* pm = a.part_m + row * a.n_parts;
+  const float* pl = a.part_l + row * a.n_parts;
+  const float4* po = reinterpret_cast<const float4*>(a.part_o + row * a.n_parts * kHeadDim) + lane;
+  constexpr int U = 8;
+  float M = -INFINITY, L = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s0 = 0; s0 < a.n_parts; s0 += U) {
+    float mv[U], lv[U];
+    float4 x[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const bool in = s0 + u < a.n_parts;
+      mv[u] = in ? pm[s0 + u] : -INFINITY;
+      lv[u] = in ? pl[s0 + u] : 0.f;
+      x[u] = in ? po[static_cast<size_t>(s0 + u) * (kHeadDim / 4)] : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    float mn = M;
+#pragma unroll
+    for (int u = 0; u < U; ++u) mn = fmaxf(mn, mv[u]);
+    const float alpha = mn == -INFINITY ? 1.f : exp2f(M - mn);
+    M = mn;
+    L *= alpha;
+    acc = make_float4(acc.x * alpha, acc.y * alpha, acc.z * alpha, acc.w * alpha);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (mv[u] == -INFINITY && lv[u] == 0.f) continue;       // a part with no token has no o
+      const float f = exp2f(mv[u] - M);
+      L = fmaf(lv[u], f, L);
+      acc = make_float4(fmaf(x[u].x, f, acc.x), fmaf(x[u].y, f, acc.y), fmaf(x[u].z, f, acc.z), fmaf(x[u].w, f, acc.w));
+    }
   }
-  store_any(a.out, a.out_dtype, row * kHeadDim + d, L == 0.f ? 0.f : acc / L);
-  if (d == 0) a.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
+  const float4 y = L == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(acc.x / L, acc.y / L, acc.z / L, acc.w / L);
+  store_four(a.out, a.out_dtype, row * kHeadDim + 4 * lane, y);
+  if (lane == 0) a.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
 }
 
 template <int RB>
@@ -255,7 +277,8 @@ cudaError_t launch_prefix_f32(const ServeArgs& a, cudaStream_t stream) {
 }
 
 cudaError_t launch_merge(const ServeArgs& a, cudaStream_t stream) {
-  merge_kernel<<<static_cast<unsigned>(a.batch) * a.n_q_heads, kHeadDim, 0, stream>>>(a);
+  const size_t rows = static_cast<size_t>(a.batch) * a.n_q_heads;
+  merge_kernel<<<static_cast<unsigned>((rows + kMergeWarps - 1) / kMergeWarps), 32 * kMergeWarps, 0, stream>>>(a);
   return cudaGetLastError();
 }
 

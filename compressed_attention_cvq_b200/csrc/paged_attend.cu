@@ -99,12 +99,7 @@ __device__ __forceinline__ void finish_row(const ServeArgs& a, size_t row, int l
   const float x[4] = {L == 0.f ? 0.f : o.x * inv, L == 0.f ? 0.f : o.y * inv,
                       L == 0.f ? 0.f : o.z * inv, L == 0.f ? 0.f : o.w * inv};
   __syncwarp();                                   // prev_lse may be lse
-  if (a.out_dtype == CVQ_F32) {
-    *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = make_float4(x[0], x[1], x[2], x[3]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) store_any(a.out, a.out_dtype, at + i, x[i]);
-  }
+  store_four(a.out, a.out_dtype, at, make_float4(x[0], x[1], x[2], x[3]));
   if (lane == 0) a.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
 }
 

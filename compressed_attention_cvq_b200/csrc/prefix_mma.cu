@@ -1,0 +1,796 @@
+// Shared-prefix attention of 16-bit queries on the tensor cores: each cached token is decoded
+// from its codes once per KV head, as fp16, straight into the operand tiles of the matrix
+// products, and read there by the query rows of every sequence.
+//
+// A CTA takes 128 query rows ((sequence, head of the group) pairs) of a KV head and a run of
+// tokens, in tiles of 64:
+//   producers (8 warps)  gather codewords from fp16 codebooks in shared memory, sum the
+//                        rounds, rotate the keys and store key and value tiles
+//   one thread           S = Q K^T (M = 128 rows, N = 64 tokens; Q from TMEM), O += P V
+//                        (N = 128 dims; P from TMEM), both tcgen05.mma kind::f16
+//   softmax (2 x 4 warps)  a thread owns a row: even tiles go to the first four warps, odd
+//                        ones to the others, each with its own O, maximum and sum (joined at
+//                        the end), so that the exponentials of one tile run under the other's
+//                        loads and barriers
+// What bounds it: exponentials (16 a clock and SM), matrix products and the producers' issue
+// slots are within 1.3 of one another for 128 rows; below that the producers.
+//
+// Bank conflicts: codebooks lie as [round][code][chunk of 8 dims], so 8 lanes that work on the
+// 8 (or 16) chunks of one token read 8 different bank groups whatever their codes are.
+//
+// Codebooks that exceed one SM (two rounds of 8-scalar groups, 64-scalar groups) are split by
+// dims over a pair of CTAs: each decodes its 64 dims of both CTAs' tokens and stores the other
+// CTA's half through distributed shared memory.
+//
+// Phases: a producer thread keeps e^{i theta t} of its 4 pairs in fp32 and turns them on from
+// token to token; every 64 tiles they are taken anew from the exact turns, which holds their
+// error below 2^-15 (2^-19 typical), far under the operands' 2^-12.
+//
+// Roundings: codewords, the rotated sum and the weights are rounded to fp16 (2^-12 at most
+// each), sums of rounds and everything after the products stay in fp32, except that two value
+// codewords (8-scalar groups) are added as fp16: that sum would be rounded to fp16 next anyhow.
+// Codebooks are scaled by a power of two into fp16's range, and so is each query row.
+#include "serve.cuh"
+
+namespace cvq {
+
+namespace {
+
+constexpr int kSoftWarps = 8;
+constexpr int kProdWarps = 8;
+constexpr int kProd = 32 * kProdWarps;
+constexpr int kThreads = 32 * (kSoftWarps + kProdWarps + 1);
+constexpr int kRows = 128;
+constexpr int kTok = 64;                          // tokens of a tile
+constexpr int kHalfTile = kTok * 128;             // 64 dims of its keys or values, bytes
+constexpr int kTile = 2 * kHalfTile;
+constexpr int kReanchor = 64;                     // tiles between exact phases
+constexpr int kOutPitch = kHeadDim + 4;           // floats; 16-byte chunks of 8 rows in 8 bank groups
+constexpr int kOutBytes = kRows * kOutPitch * 4;
+// columns of TMEM: S of the two streams, their P (two fp16 a column), Q, their O
+constexpr uint32_t kColS = 0, kColP = 128, kColQ = 192, kColO = 256, kTmemCols = 512;
+
+struct Control {
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], pv_done[2];
+  uint32_t tmem;
+  alignas(8) uint32_t peak[2][2];                 // [CTA of the pair][keys, values], bits of |x|
+  uint32_t warp_peak[2][kThreads / 32];
+  float m[kRows], l[kRows];                       // second stream's state
+};
+
+// ---- PTX ----
+__device__ __forceinline__ bool wait(uint64_t* bar, unsigned parity, unsigned int* fault) {
+  const uint32_t addr = smem_u32(bar);
+  unsigned long long t0 = 0;
+  for (int i = 0;; ++i) {
+    uint32_t done;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n"
+        " selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(done) : "r"(addr), "r"(parity), "r"(kMbarSuspendHintNs) : "memory");
+    if (done) return true;
+    unsigned long long now;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
+    if (i == 0) t0 = now;
+    else if (now - t0 > kMbarWaitLimitNs) {
+      atomicOr(fault, kFaultCopyTimeout);
+      return false;
+    }
+  }
+}
+__device__ __forceinline__ void arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ uint32_t map_to(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void arrive_at(uint64_t* bar, uint32_t rank) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(map_to(smem_u32(bar), rank)) : "memory");
+}
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+template <int C>
+__device__ __forceinline__ void commit(uint64_t* bar, bool both) {
+  if (C == 2 && both) {
+    asm volatile(
+        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_u32(bar)),
+        "h"(static_cast<uint16_t>(3)) : "memory");
+  } else {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+  }
+}
+__device__ __forceinline__ void mma_f16(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d), "r"(a), "l"(b), "r"(idesc),
+      "r"(static_cast<uint32_t>(acc)) : "memory");
+}
+#define CVQ_R4(x, i) "=r"(x[i]), "=r"(x[i + 1]), "=r"(x[i + 2]), "=r"(x[i + 3])
+#define CVQ_V4(x, i) "r"(x[i]), "r"(x[i + 1]), "r"(x[i + 2]), "r"(x[i + 3])
+__device__ __forceinline__ void tmem_load32(uint32_t (&r)[32], uint32_t at) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : CVQ_R4(r, 0), CVQ_R4(r, 4), CVQ_R4(r, 8), CVQ_R4(r, 12), CVQ_R4(r, 16), CVQ_R4(r, 20), CVQ_R4(r, 24), CVQ_R4(r, 28)
+      : "r"(at) : "memory");
+}
+__device__ __forceinline__ void tmem_store32(uint32_t at, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::CVQ_V4(r, 0), CVQ_V4(r, 4), CVQ_V4(r, 8), CVQ_V4(r, 12),
+      CVQ_V4(r, 16), CVQ_V4(r, 20), CVQ_V4(r, 24), CVQ_V4(r, 28), "r"(at) : "memory");
+}
+__device__ __forceinline__ void tmem_load_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_before_sync() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tmem_after_sync() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+// operand descriptor: 128-byte swizzle, `lead` and `stride` bytes (see the tiles' layouts below)
+__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t lead, uint32_t stride) {
+  return static_cast<uint64_t>((addr >> 4) & 0x3fffu) | (static_cast<uint64_t>(lead >> 4) << 16) |
+         (static_cast<uint64_t>(stride >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+__device__ __forceinline__ uint4 lds16(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ void sts16(uint32_t addr, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ void sts16_cluster(uint32_t addr, uint4 v) {
+  asm volatile("st.shared::cluster.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+// pairs of fp32 numbers in one instruction
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 pack(float x, float y) {
+  f2 r;
+  asm("mov.b64 %0, {%1,%2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 unpack(f2 v) {
+  float2 r;
+  asm("mov.b64 {%0,%1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ f2 mul2(f2 x, f2 y) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+  return r;
+}
+__device__ __forceinline__ f2 fma2(f2 x, f2 y, f2 z) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+  return r;
+}
+__device__ __forceinline__ f2 add2(f2 x, f2 y) {
+  f2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+  return r;
+}
+__device__ __forceinline__ f2 neg2(f2 x) { return x ^ 0x8000000080000000ull; }
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t half_pair(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float2 floats_of(uint32_t h) { return __half22float2(*reinterpret_cast<const __half2*>(&h)); }
+__device__ __forceinline__ uint32_t add_halves(uint32_t x, uint32_t y) {
+  const __half2 h = __hadd2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&y));
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// x[8] += the 8 fp16 numbers of v
+__device__ __forceinline__ void add_chunk(float (&x)[8], uint4 v) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    asm("add.f32.f16 %0, %1, %0;" : "+f"(x[2 * i]) : "h"(static_cast<uint16_t>(w[i] & 0xffffu)));
+    asm("add.f32.f16 %0, %1, %0;" : "+f"(x[2 * i + 1]) : "h"(static_cast<uint16_t>(w[i] >> 16)));
+  }
+}
+__device__ __forceinline__ void set_chunk(float (&x)[8], uint4 v) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = floats_of(w[i]);
+    x[2 * i] = f.x;
+    x[2 * i + 1] = f.y;
+  }
+}
+
+// e^{i theta_j t} of the 4 pairs of a chunk; packed two pairs at a time
+struct Phase {
+  f2 c[2], s[2];
+  __device__ __forceinline__ void set(const PhaseTurns& ph, int chunk, unsigned long long t) {
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      const float2 x = phase_exact(ph.F[4 * chunk + 2 * p] * t), y = phase_exact(ph.F[4 * chunk + 2 * p + 1] * t);
+      c[p] = pack(x.x, y.x);
+      s[p] = pack(x.y, y.y);
+    }
+  }
+  __device__ __forceinline__ void turn(const Phase& w) {
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      const f2 nc = fma2(neg2(s[p]), w.s[p], mul2(c[p], w.c[p]));
+      s[p] = fma2(s[p], w.c[p], mul2(c[p], w.s[p]));
+      c[p] = nc;
+    }
+  }
+  // 8 dims (4 interleaved pairs) rotated and rounded
+  __device__ __forceinline__ uint4 rotate(const float (&x)[8]) const {
+    uint32_t w[4];
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      const f2 re = pack(x[4 * p], x[4 * p + 2]), im = pack(x[4 * p + 1], x[4 * p + 3]);
+      const float2 a = unpack(fma2(im, neg2(s[p]), mul2(re, c[p]))), b = unpack(fma2(im, c[p], mul2(re, s[p])));
+      w[2 * p] = half_pair(a.x, b.x);
+      w[2 * p + 1] = half_pair(a.y, b.y);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
+
+// ---- codebooks to shared memory ----
+// One CTA's share of a KV head's codebook as fp16 times `scale`; returns the bits of the
+// largest finite |x| that this thread saw.
+template <int C, bool kWide>
+__device__ __forceinline__ uint32_t stage_codebook(const float* cb, uint32_t dst, int R, int rank, float scale) {
+  constexpr int CH = 16 / C;                      // chunks of 8 dims that this CTA holds
+  const int n = kWide ? R * kWideCodes * 8 : R * kCodes * CH;
+  uint32_t peak = 0;
+#pragma unroll 4
+  for (int i = threadIdx.x; i < n; i += kThreads) {
+    const float* src;
+    if (kWide) {
+      src = cb + (static_cast<size_t>(rank) * R * kWideCodes * 8 + i) * 8;
+    } else {
+      const int chunk = i % CH + (C == 2 ? 8 * rank : 0), e = i / CH;      // e = round * 256 + code
+      src = cb + (static_cast<size_t>(chunk) * R * kCodes + e) * 8;
+    }
+    const float4 x = __ldg(reinterpret_cast<const float4*>(src)), y = __ldg(reinterpret_cast<const float4*>(src) + 1);
+    const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+    for (int d = 0; d < 8; ++d) {
+      const uint32_t bits = __float_as_uint(v[d]) & 0x7fffffffu;
+      if (bits < 0x7f800000u) peak = max(peak, bits);
+    }
+    sts16(dst + i * 16, make_uint4(half_pair(v[0] * scale, v[1] * scale), half_pair(v[2] * scale, v[3] * scale),
+                                   half_pair(v[4] * scale, v[5] * scale), half_pair(v[6] * scale, v[7] * scale)));
+  }
+  return peak;
+}
+
+// Exponent of the codebook scale: 6 wherever the decoded numbers then lie well inside fp16's
+// range, so that one reading of the codebook is enough; else what takes the largest to 2^14.
+constexpr int kUsualScale = 6;
+__device__ __forceinline__ int scale_exponent(uint32_t peak_bits, int R) {
+  const float most = __uint_as_float(peak_bits) * static_cast<float>(R) * 1.5f;      // 1.5 > sqrt 2: rotated
+  if (peak_bits == 0 || (most < 512.f && most > 0.0078125f)) return kUsualScale;
+  return min(max(14 - ilogbf(fminf(most, 3e38f)), -120), 120);
+}
+
+// two 16-bit query elements as floats
+__device__ __forceinline__ float2 query_pair(uint32_t w, bool bf16) {
+  return bf16 ? make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)) : floats_of(w);
+}
+
+// kWide: R is the most rounds; the call's own number is a.R
+template <int C, bool kWide, int R>
+__global__ void __launch_bounds__(kThreads, 1) prefix_mma_kernel(const __grid_constant__ ServeArgs a) {
+  constexpr int kGroupTok = C * kTok;             // tokens of a step of the CTA or pair
+  constexpr int CH = 16 / C;
+  constexpr int kSlots = kProd / CH;              // tokens that the producers take at once; 4 in turn
+  constexpr int kVStages = kWide ? 1 : 2;
+  static_assert(kSlots * 4 == kGroupTok, "a producer thread takes 4 tokens a step");
+  static_assert(!kWide || C == 2, "a CTA holds one 64-scalar group");
+  extern __shared__ __align__(1024) unsigned char smem[];
+  const uint32_t tiles_k = smem_u32(smem), tiles_v = tiles_k + 2 * kTile;
+  const uint32_t cb_k = tiles_v + kVStages * kTile;
+  const int rounds = kWide ? a.R : R;
+  const uint32_t cb_bytes = kWide ? rounds * kWideCodes * 128 : R * kCodes * CH * 16;
+  const uint32_t cb_v = cb_k + cb_bytes;
+  const uint32_t ctl_at = max(cb_v + cb_bytes - tiles_k, static_cast<uint32_t>(kOutBytes));
+  Control& ctl = *reinterpret_cast<Control*>(smem + ctl_at);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = C == 2 ? static_cast<int>(blockIdx.x & 1) : 0;
+  const int split = blockIdx.x / C, h = blockIdx.y;
+  const int r0 = blockIdx.z * kRows;
+  const int nrows = min(kRows, a.batch * a.group - r0);
+  const int nact = (nrows + 31) / 32;             // softmax warps with rows, of each stream
+  const size_t n_parts = static_cast<size_t>(a.n_parts);
+  auto global_row = [&](int r) {
+    const int rr = r0 + r;
+    return static_cast<size_t>(rr / a.group) * a.n_q_heads + static_cast<size_t>(h) * a.group + rr % a.group;
+  };
+  int L = a.lens[0];
+  L = L < 0 ? 0 : (L > a.t_cap ? a.t_cap : L);
+  const long long per = ((L + a.n_splits - 1LL) / a.n_splits + kGroupTok - 1) / kGroupTok * kGroupTok;
+  const long long start = min(per * split, static_cast<long long>(L)), end = min(start + per, static_cast<long long>(L));
+  const int ntiles = static_cast<int>((end - start + kGroupTok - 1) / kGroupTok);
+  if (ntiles == 0) {                              // the same for both CTAs of a pair
+    if (threadIdx.x < nrows) {
+      const size_t at = global_row(threadIdx.x) * n_parts + blockIdx.x;
+      a.part_m[at] = -INFINITY;
+      a.part_l[at] = 0.f;
+    }
+    return;
+  }
+
+  // ---- set-up ----
+  if (C == 2) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  if (warp == kSoftWarps + kProdWarps) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&ctl.tmem)), "r"(kTmemCols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    if (lane == 0) {
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        mbar_init(&ctl.k_full[s], kProdWarps * C);
+        mbar_init(&ctl.v_full[s], kProdWarps * C);
+        mbar_init(&ctl.k_empty[s], C);
+        mbar_init(&ctl.v_empty[s], C);
+        mbar_init(&ctl.s_full[s], 1);
+        mbar_init(&ctl.p_full[s], nact);
+        mbar_init(&ctl.pv_done[s], 1);
+      }
+    }
+  }
+  const float* kcb = a.key_cb + static_cast<long long>(h) * a.key_cb_stride;
+  const float* vcb = a.val_cb + static_cast<long long>(h) * a.val_cb_stride;
+  constexpr float kUsual = static_cast<float>(1 << kUsualScale);
+  uint32_t pk = stage_codebook<C, kWide>(kcb, cb_k, rounds, rank, kUsual);
+  uint32_t pv = stage_codebook<C, kWide>(vcb, cb_v, rounds, rank, kUsual);
+  pk = __reduce_max_sync(0xffffffffu, pk);
+  pv = __reduce_max_sync(0xffffffffu, pv);
+  if (lane == 0) {
+    ctl.warp_peak[0][warp] = pk;
+    ctl.warp_peak[1][warp] = pv;
+  }
+  tmem_before_sync();
+  __syncthreads();
+  tmem_after_sync();
+  pk = __reduce_max_sync(0xffffffffu, lane < kThreads / 32 ? ctl.warp_peak[0][lane] : 0u);
+  pv = __reduce_max_sync(0xffffffffu, lane < kThreads / 32 ? ctl.warp_peak[1][lane] : 0u);
+  if (C == 2) {
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");            // the other CTA runs
+    if (threadIdx.x == 0) {
+#pragma unroll
+      for (uint32_t to = 0; to < 2; ++to) {
+        const uint32_t at = map_to(smem_u32(&ctl.peak[rank][0]), to);
+        asm volatile("st.shared::cluster.v2.u32 [%0], {%1,%2};" ::"r"(at), "r"(pk), "r"(pv) : "memory");
+      }
+    }
+    __syncwarp();
+    cluster_barrier();                            // barriers and peaks of both CTAs are there
+    pk = max(ctl.peak[0][0], ctl.peak[1][0]);
+    pv = max(ctl.peak[0][1], ctl.peak[1][1]);
+  }
+  const int ek = scale_exponent(pk, rounds), ev = scale_exponent(pv, rounds);
+  if (ek != kUsualScale) stage_codebook<C, kWide>(kcb, cb_k, rounds, rank, ldexpf(1.f, ek));
+  if (ev != kUsualScale) stage_codebook<C, kWide>(vcb, cb_v, rounds, rank, ldexpf(1.f, ev));
+  const uint32_t tmem = ctl.tmem;
+
+  // query rows: scale of each (both streams), and the operand (first stream)
+  float factor = 0.f;
+  if (warp < kSoftWarps && (warp & 3) < nact) {
+    const int r = (warp & 3) * 32 + lane;
+    const bool bf16 = a.q_dtype == CVQ_BF16;
+    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + global_row(min(r, nrows - 1)) * kHeadDim);
+    float mx = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const uint4 v = __ldg(src + i);
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 f = query_pair(w[j], bf16);
+        mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
+      }
+    }
+    // largest element to [2^8, 2^9)
+    const int eq = mx > 0.f && mx < INFINITY ? 8 - ilogbf(mx) : 0;
+    factor = ldexpf(0.08838834764831845f * kLog2e, -eq - ek);
+    if (warp < 4) {
+      const float up = ldexpf(1.f, min(eq, 127)), rest = ldexpf(1.f, eq - min(eq, 127));
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t out[32];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint4 v = __ldg(src + half * 8 + i);
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 f = query_pair(w[j], bf16);
+            out[4 * i + j] = r < nrows ? half_pair(f.x * up * rest, f.y * up * rest) : 0u;
+          }
+        }
+        tmem_store32(tmem + (static_cast<uint32_t>(warp * 32) << 16) + kColQ + half * 32, out);
+      }
+      tmem_store_wait();
+    }
+  }
+  tmem_before_sync();
+  __syncthreads();
+  tmem_after_sync();
+
+  float m = -INFINITY, l = 0.f;                   // softmax: log2 maximum and sum of this thread's row
+  if (warp < kSoftWarps) {
+    // ================= softmax =================
+    const int st = warp >> 2, q4 = warp & 3;
+    const uint32_t lanes = tmem + (static_cast<uint32_t>(q4 * 32) << 16);
+    // weights are 2^(s - m + kLift); m is followed only when it grows by kSlack, so that O is
+    // rescaled a few times and not at every tile, and weights stay below 2^(kLift + kSlack)
+    constexpr float kLift = 7.f, kSlack = 8.f;
+    if (q4 < nact) {
+      for (int i = st; i < ntiles; i += 2) {
+        const unsigned par = (i >> 1) & 1;
+        if (!wait(&ctl.s_full[st], par, a.fault)) break;
+        tmem_after_sync();
+        uint32_t s0[32], s1[32];
+        tmem_load32(s0, lanes + kColS + st * kTok);
+        tmem_load32(s1, lanes + kColS + st * kTok + 32);
+        tmem_load_wait();
+        const long long left = end - (start + static_cast<long long>(i) * kGroupTok + rank * kTok);
+        if (left < kTok) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            if (j >= left) s0[j] = 0xff800000u;
+            if (j + 32 >= left) s1[j] = 0xff800000u;
+          }
+        }
+        float mx = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) mx = fmaxf(mx, fmaxf(__uint_as_float(s0[j]), __uint_as_float(s1[j])));
+        mx *= factor;
+        const bool grow = mx > m + kSlack || (m == -INFINITY && mx > m);
+        const float alpha = grow ? exp2f(m - mx) : 1.f;
+        if (grow) m = mx;
+        const float ref = m == -INFINITY ? 0.f : m - kLift;
+        const f2 ff = pack(factor, factor), rr = pack(-ref, -ref);
+        f2 sum = 0;
+        uint32_t p[32];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const float2 x = unpack(fma2(pack(__uint_as_float(s0[2 * j]), __uint_as_float(s0[2 * j + 1])), ff, rr));
+          const float2 y = unpack(fma2(pack(__uint_as_float(s1[2 * j]), __uint_as_float(s1[2 * j + 1])), ff, rr));
+          const float e0 = exp2_fast(x.x), e1 = exp2_fast(x.y), e2 = exp2_fast(y.x), e3 = exp2_fast(y.y);
+          sum = add2(sum, add2(pack(e0, e1), pack(e2, e3)));
+          p[j] = half_pair(e0, e1);
+          p[16 + j] = half_pair(e2, e3);
+        }
+        const float2 sums = unpack(sum);
+        l = fmaf(l, alpha, sums.x + sums.y);
+        if (i >= 2) {
+          if (!wait(&ctl.pv_done[st], par ^ 1, a.fault)) break;
+          tmem_after_sync();
+          if (__any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              uint32_t o[32];
+              tmem_load32(o, lanes + kColO + st * kHeadDim + 32 * c);
+              tmem_load_wait();
+#pragma unroll
+              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
+              tmem_store32(lanes + kColO + st * kHeadDim + 32 * c, o);
+            }
+          }
+        }
+        tmem_store32(lanes + kColP + st * 32, p);
+        tmem_store_wait();
+        tmem_before_sync();
+        __syncwarp();
+        if (lane == 0) arrive(&ctl.p_full[st]);
+      }
+      // the last product of this stream
+      const int n = (ntiles - st + 1) / 2;
+      if (n > 0) wait(&ctl.pv_done[st], (n - 1) & 1, a.fault);
+      tmem_after_sync();
+    }
+    if (m != -INFINITY) m -= kLift;
+  } else if (warp < kSoftWarps + kProdWarps) {
+    // ================= producers =================
+    const int tid = threadIdx.x - 32 * kSoftWarps;
+    const int cl = tid % CH, slot = tid / CH;
+    const int chunk = C == 2 ? 8 * rank + cl : cl;
+    // token u of this thread within a step, the CTA it belongs to and its row of the tile there
+    auto token = [&](int u) { return kWide ? 4 * slot + u : slot + u * kSlots; };
+    uint32_t at[4];                               // of its 16 bytes, from the start of a tile
+    bool mine[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int row = token(u) % kTok, to = C == 2 ? token(u) / kTok : 0;
+      mine[u] = to == rank;
+      at[u] = (chunk >> 3) * kHalfTile + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);
+      if (!mine[u]) at[u] = map_to(tiles_k + at[u], static_cast<uint32_t>(to)) - tiles_k;
+    }
+    auto store = [&](uint32_t tile, int u, uint4 v) {
+      if (C == 1 || mine[u]) sts16(tile + at[u], v);
+      else sts16_cluster(tile + at[u], v);
+    };
+    auto publish = [&](uint64_t* bar) {
+      if (C == 2) asm volatile("fence.proxy.async;" ::: "memory");
+      else fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        if (C == 2) {
+          arrive_at(bar, 0);
+          arrive_at(bar, 1);
+        } else {
+          arrive(bar);
+        }
+      }
+    };
+    Phase ph, step, jump;
+    step.set(a.phase, chunk, kWide ? 1 : kSlots);
+    if (kWide) jump.set(a.phase, chunk, kGroupTok - 3);
+    const uint32_t my_k = cb_k + cl * 16, my_v = cb_v + cl * 16;
+    // codes of a step: one byte per (token, round), or a word of 4 tokens per round
+    constexpr int kWords = kWide ? R : 4 * R;
+    uint32_t wk[kWords], wv[kWords];
+    auto load_codes = [&](const uint8_t* codes, uint32_t (&w)[kWords], int i) {
+      const long long t0 = start + static_cast<long long>(i) * kGroupTok;
+      if constexpr (kWide) {
+        const long long t = t0 + 4 * slot;
+        const size_t row_bytes = a.code_bits == 6 ? static_cast<size_t>(a.t_cap) / 4 * 3 : static_cast<size_t>(a.t_cap);
+        const uint8_t* p = codes + (static_cast<size_t>(h) * kWideGroups + rank) * rounds * row_bytes +
+                           (a.code_bits == 6 ? t / 4 * 3 : t);
+        const bool in = t < end;                  // rows are whole words: t .. t + 3 lie inside
+        // packed: the 24 bits from p, out of one or two aligned words
+        const unsigned shift = a.code_bits == 6 ? (reinterpret_cast<uintptr_t>(p) & 3) * 8 : 0;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          if (r < rounds && in) {
+            const uint8_t* q = p + r * row_bytes;
+            // rows of 3 t_cap / 4 bytes, t_cap a multiple of 64: every row has p's alignment
+            const uint32_t* word = reinterpret_cast<const uint32_t*>(q - (shift >> 3));
+            const uint32_t lo = __ldg(word), hi = shift > 8 ? __ldg(word + 1) : 0u;
+            w[r] = __funnelshift_r(lo, hi, shift);
+          } else {
+            w[r] = 0u;
+          }
+        }
+      } else {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const long long t = min(t0 + token(u), end - 1);
+          const uint8_t* p = codes + ((static_cast<size_t>(h) * a.t_cap + t) * R) * kGroups + chunk;
+#pragma unroll
+          for (int r = 0; r < R; ++r) w[u * R + r] = __ldg(p + r * kGroups);
+        }
+      }
+    };
+    // offset of the codeword of word w and token u within a round of a codebook
+    const int unit = a.code_bits == 6 ? 6 : 8;
+    auto entry = [&](uint32_t w, int u) { return ((w >> (unit * u)) & 63u) * 128u; };
+    auto make_keys = [&](int i) {
+      const int s = i & 1;
+      if (i >= 2 && !wait(&ctl.k_empty[s], ((i >> 1) - 1) & 1, a.fault)) return false;
+      const uint32_t tile = tiles_k + s * kTile;
+      if (i % kReanchor == 0)
+        ph.set(a.phase, chunk, static_cast<unsigned long long>(start + static_cast<long long>(i) * kGroupTok + token(0)));
+      if constexpr (kWide) {
+#pragma unroll
+        for (int u = 0; u < 4; u += 2) {
+          float x[2][8];
+#pragma unroll
+          for (int d = 0; d < 8; ++d) x[0][d] = x[1][d] = 0.f;
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            if (r < rounds) {
+              add_chunk(x[0], lds16(my_k + r * (kWideCodes * 128) + entry(wk[r], u)));
+              add_chunk(x[1], lds16(my_k + r * (kWideCodes * 128) + entry(wk[r], u + 1)));
+            }
+          }
+          store(tile, u, ph.rotate(x[0]));
+          ph.turn(step);
+          store(tile, u + 1, ph.rotate(x[1]));
+          if (u == 0) ph.turn(step);
+          else ph.turn(jump);
+        }
+      } else {
+        uint4 v[4 * R];
+#pragma unroll
+        for (int j = 0; j < 4 * R; ++j) v[j] = lds16(my_k + (j % R) * (kCodes * CH * 16) + wk[j] * (CH * 16));
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          float x[8];
+          set_chunk(x, v[u * R]);
+#pragma unroll
+          for (int r = 1; r < R; ++r) add_chunk(x, v[u * R + r]);
+          store(tile, u, ph.rotate(x));
+          ph.turn(step);
+        }
+      }
+      publish(&ctl.k_full[s]);
+      if (i + 1 < ntiles) load_codes(a.key_codes, wk, i + 1);
+      return true;
+    };
+    auto make_values = [&](int i) {
+      const int s = kVStages == 2 ? i & 1 : 0, lap = i / kVStages;
+      if (lap > 0 && !wait(&ctl.v_empty[s], (lap - 1) & 1, a.fault)) return false;
+      const uint32_t tile = tiles_v + s * kTile;
+      const long long left = end - (start + static_cast<long long>(i) * kGroupTok);
+      uint4 v[4];
+      if constexpr (kWide) {
+#pragma unroll
+        for (int u = 0; u < 4; u += 2) {
+          float x[2][8];
+#pragma unroll
+          for (int d = 0; d < 8; ++d) x[0][d] = x[1][d] = 0.f;
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            if (r < rounds) {
+              add_chunk(x[0], lds16(my_v + r * (kWideCodes * 128) + entry(wv[r], u)));
+              add_chunk(x[1], lds16(my_v + r * (kWideCodes * 128) + entry(wv[r], u + 1)));
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            v[u + k] = make_uint4(half_pair(x[k][0], x[k][1]), half_pair(x[k][2], x[k][3]), half_pair(x[k][4], x[k][5]),
+                                  half_pair(x[k][6], x[k][7]));
+        }
+      } else {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          v[u] = lds16(my_v + wv[u * R] * (CH * 16));
+#pragma unroll
+          for (int r = 1; r < R; ++r) {
+            const uint4 y = lds16(my_v + r * (kCodes * CH * 16) + wv[u * R + r] * (CH * 16));
+            v[u] = make_uint4(add_halves(v[u].x, y.x), add_halves(v[u].y, y.y), add_halves(v[u].z, y.z), add_halves(v[u].w, y.w));
+          }
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        if (token(u) >= left) v[u] = make_uint4(0u, 0u, 0u, 0u);            // weight 0 times this must be 0
+        store(tile, u, v[u]);
+      }
+      publish(&ctl.v_full[s]);
+      if (i + 1 < ntiles) load_codes(a.val_codes, wv, i + 1);
+      return true;
+    };
+    load_codes(a.key_codes, wk, 0);
+    load_codes(a.val_codes, wv, 0);
+    bool ok = make_keys(0);                       // keys run one tile ahead of the values
+    for (int i = 0; ok && i < ntiles; ++i) {
+      if (i + 1 < ntiles) ok = make_keys(i + 1);
+      ok = ok && make_values(i);
+    }
+  } else if (lane == 0) {
+    // ================= matrix products =================
+    // A tile is two halves of 64 dims, each [64 tokens][128 bytes] with 16-byte chunk c of row t
+    // at c ^ (t & 7).  As keys (N = tokens, K = dims, K-major) 8 rows are 1024 bytes apart and 16
+    // dims 32 bytes; as values (N = dims, K = tokens, N-major) 64 dims are a half apart and 8
+    // tokens 1024 bytes.
+    constexpr uint32_t kDescS = (1u << 4) | ((kTok >> 3) << 17) | ((kRows >> 4) << 24);
+    constexpr uint32_t kDescO = (1u << 4) | (1u << 16) | ((kHeadDim >> 3) << 17) | ((kRows >> 4) << 24);
+    for (int i = 0; i <= ntiles; ++i) {
+      if (i < ntiles) {
+        const int s = i & 1;
+        if (!wait(&ctl.k_full[s], (i >> 1) & 1, a.fault)) break;
+        asm volatile("fence.proxy.async;" ::: "memory");
+        tmem_after_sync();
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          mma_f16(tmem + kColS + s * kTok, tmem + kColQ + 8 * k,
+                  operand(tiles_k + s * kTile + (k >> 2) * kHalfTile + (k & 3) * 32, 16, 1024), kDescS, k > 0);
+        commit<C>(&ctl.s_full[s], false);
+        if (i + 2 < ntiles) commit<C>(&ctl.k_empty[s], true);
+      }
+      if (i > 0) {
+        const int j = i - 1, st = j & 1, s = kVStages == 2 ? st : 0;
+        if (!wait(&ctl.v_full[s], (j / kVStages) & 1, a.fault)) break;
+        if (!wait(&ctl.p_full[st], (j >> 1) & 1, a.fault)) break;
+        asm volatile("fence.proxy.async;" ::: "memory");
+        tmem_after_sync();
+#pragma unroll
+        for (int k = 0; k < kTok / 16; ++k)
+          mma_f16(tmem + kColO + st * kHeadDim, tmem + kColP + st * 32 + 8 * k,
+                  operand(tiles_v + s * kTile + k * 2048, kHalfTile, 1024), kDescO, j >= 2 || k > 0);
+        if (j + kVStages < ntiles) commit<C>(&ctl.v_empty[s], true);
+        commit<C>(&ctl.pv_done[st], false);
+      }
+    }
+  }
+  __syncwarp();
+  __syncthreads();                                // tiles and codebooks are no longer read
+
+  // ---- join the two streams and write this CTA's partial state ----
+  float* rows_out = reinterpret_cast<float*>(smem);
+  const int r = (warp & 3) * 32 + lane;
+  const bool second = ntiles > 1;
+  if (second && warp >= 4 && warp < kSoftWarps && (warp & 3) < nact) {
+    ctl.m[r] = m;
+    ctl.l[r] = l;
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+      uint32_t o[32];
+      tmem_load32(o, tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + kColO + kHeadDim + 32 * c);
+      tmem_load_wait();
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        *reinterpret_cast<uint4*>(rows_out + r * kOutPitch + 32 * c + 4 * j) = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+    }
+  }
+  __syncthreads();
+  if (warp < nact) {
+    const float m1 = second ? ctl.m[r] : -INFINITY, l1 = second ? ctl.l[r] : 0.f;
+    const float M = fmaxf(m, m1), ref = M == -INFINITY ? 0.f : M;
+    const float f0 = exp2f(m - ref), f1 = exp2f(m1 - ref);
+    const float back = ldexpf(1.f, -ev);
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+      uint32_t o[32];
+      tmem_load32(o, tmem + (static_cast<uint32_t>(warp * 32) << 16) + kColO + 32 * c);
+      tmem_load_wait();
+#pragma unroll
+      for (int j = 0; j < 32; j += 4) {
+        float4* at = reinterpret_cast<float4*>(rows_out + r * kOutPitch + 32 * c + j);
+        float4 x = second ? *at : make_float4(0.f, 0.f, 0.f, 0.f);
+        x.x = fmaf(__uint_as_float(o[j]), f0, x.x * f1) * back;
+        x.y = fmaf(__uint_as_float(o[j + 1]), f0, x.y * f1) * back;
+        x.z = fmaf(__uint_as_float(o[j + 2]), f0, x.z * f1) * back;
+        x.w = fmaf(__uint_as_float(o[j + 3]), f0, x.w * f1) * back;
+        *at = x;
+      }
+    }
+    if (r < nrows) {
+      const size_t at = global_row(r) * n_parts + blockIdx.x;
+      a.part_m[at] = M;
+      a.part_l[at] = fmaf(l, f0, l1 * f1);
+    }
+  }
+  tmem_before_sync();
+  __syncthreads();
+  for (int i = threadIdx.x; i < nrows * 32; i += kThreads) {
+    const int rr = i >> 5, c = (i & 31) * 4;
+    *reinterpret_cast<float4*>(a.part_o + (global_row(rr) * n_parts + blockIdx.x) * kHeadDim + c) =
+        *reinterpret_cast<const float4*>(rows_out + rr * kOutPitch + c);
+  }
+  if (warp == kSoftWarps + kProdWarps)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+  if (C == 2) cluster_barrier();                  // the other CTA may still store here until now
+}
+
+template <int C, bool kWide, int R>
+cudaError_t run(const ServeArgs& a, cudaStream_t stream) {
+  static PerDeviceFlag flag;
+  constexpr int kTiles = (kWide ? 3 : 4) * kTile;
+  constexpr size_t kMost = kTiles + (kWide ? 2u * R * kWideCodes * 128 : 2u * R * kCodes * (16 / C) * 16) + sizeof(Control);
+  static_assert(kMost <= 227 * 1024, "fits an SM");
+  cudaError_t e = set_smem_limit_once(flag, prefix_mma_kernel<C, kWide, R>, kMost);
+  if (e != cudaSuccess) return e;
+  size_t bytes = kTiles + (kWide ? 2u * a.R * kWideCodes * 128 : 2u * R * kCodes * (16 / C) * 16);
+  if (bytes < kOutBytes) bytes = kOutBytes;
+  bytes += sizeof(Control);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = C;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(a.n_splits * C, a.n_kv_heads, (a.batch * a.group + kRows - 1) / kRows);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = bytes;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, prefix_mma_kernel<C, kWide, R>, a);
+}
+
+}  // namespace
+
+cudaError_t launch_prefix_mma(const ServeArgs& a, cudaStream_t stream) {
+  if (a.wide) return run<2, true, kWideRoundsPerCta>(a, stream);
+  return a.R == 1 ? run<1, false, 1>(a, stream) : run<2, false, 2>(a, stream);
+}
+
+}  // namespace cvq

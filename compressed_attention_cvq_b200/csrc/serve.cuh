@@ -19,6 +19,7 @@ struct ServeArgs {
   int q_dtype;
   int batch, n_q_heads, n_kv_heads, group;
   int n_splits, split_tokens;
+  int n_parts;                    // partial states per row: n_splits, or one per CTA of its pairs
   float* part_o;
   float* part_m;
   float* part_l;
@@ -70,10 +71,20 @@ __device__ __forceinline__ float load_any(const void* p, int dtype, size_t i) {
   if (dtype == CVQ_F16) return __half2float(static_cast<const __half*>(p)[i]);
   return static_cast<const float*>(p)[i];
 }
-__device__ __forceinline__ void store_any(void* p, int dtype, size_t i, float x) {
-  if (dtype == CVQ_BF16) static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(x);
-  else if (dtype == CVQ_F16) static_cast<__half*>(p)[i] = __float2half_rn(x);
-  else static_cast<float*>(p)[i] = x;
+
+// four elements from i on (a multiple of 4)
+__device__ __forceinline__ void store_four(void* p, int dtype, size_t i, float4 x) {
+  if (dtype == CVQ_F32) {
+    *reinterpret_cast<float4*>(static_cast<float*>(p) + i) = x;
+  } else if (dtype == CVQ_BF16) {
+    __nv_bfloat162* at = reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(p) + i);
+    at[0] = __floats2bfloat162_rn(x.x, x.y);
+    at[1] = __floats2bfloat162_rn(x.z, x.w);
+  } else {
+    __half2* at = reinterpret_cast<__half2*>(static_cast<__half*>(p) + i);
+    at[0] = __floats2half2_rn(x.x, x.y);
+    at[1] = __floats2half2_rn(x.z, x.w);
+  }
 }
 
 // e^{2 pi i turn64 / 2^64} to full fp32 accuracy (phase_from_turn's __sincosf is good to
@@ -91,6 +102,7 @@ cvq_status check_shape_status(const cvq_shape* s);
 cvq_status check_codebook_stride(const cvq_shape* s, int64_t stride);
 
 cudaError_t launch_prefix_f32(const ServeArgs& a, cudaStream_t stream);
+cudaError_t launch_prefix_mma(const ServeArgs& a, cudaStream_t stream);   // 16-bit queries
 cudaError_t launch_paged_attend(const ServeArgs& a, cudaStream_t stream);
 cudaError_t launch_merge(const ServeArgs& a, cudaStream_t stream);
 cudaError_t launch_paged_append(const AppendArgs& a, int in_dtype, int kv_dtype, cudaStream_t stream);

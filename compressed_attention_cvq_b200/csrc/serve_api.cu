@@ -29,14 +29,21 @@ int dtype_bytes(int d) { return d == CVQ_F32 ? 4 : 2; }
 bool is_wide(const cvq_shape* s) { return s->group_dim == kWideGroupDim; }
 size_t round16(size_t n) { return (n + 15) / 16 * 16; }
 
+// CTAs of the tensor-core kernel that share a split (each leaves a partial state), and whether
+// it takes the call: 16-bit queries, and rounds whose codebooks fit a pair of SMs
+int prefix_pair(const cvq_shape* s) { return !is_wide(s) && s->R == 1 ? 1 : 2; }
+bool prefix_on_tensor_cores(const cvq_shape* s, int q_dtype) {
+  return q_dtype != CVQ_F32 && (!is_wide(s) || s->R <= kWideRoundsPerCta);
+}
+
 // partial states and one arrival counter per (sequence, query head)
-size_t workspace_bytes(int batch, int n_q_heads, int n_splits) {
+size_t workspace_bytes(int batch, int n_q_heads, int n_parts) {
   const size_t rows = static_cast<size_t>(batch) * n_q_heads;
-  return round16(rows * n_splits * (kHeadDim + 2) * sizeof(float)) + round16(rows * sizeof(int));
+  return round16(rows * n_parts * (kHeadDim + 2) * sizeof(float)) + round16(rows * sizeof(int));
 }
 
 void place_workspace(ServeArgs& a, void* workspace) {
-  const size_t rows = static_cast<size_t>(a.batch) * a.n_q_heads * a.n_splits;
+  const size_t rows = static_cast<size_t>(a.batch) * a.n_q_heads * a.n_parts;
   a.part_o = static_cast<float*>(workspace);
   a.part_m = a.part_o + rows * kHeadDim;
   a.part_l = a.part_m + rows;
@@ -86,12 +93,18 @@ extern "C" {
 
 size_t cvq_prefix_workspace_bytes(const cvq_shape* s, int n_splits) {
   if (cvq_partials_bytes(s, n_splits) == 0) return 0;
-  return workspace_bytes(s->batch, s->n_q_heads, n_splits);
+  return workspace_bytes(s->batch, s->n_q_heads, n_splits * prefix_pair(s));
 }
 
 int cvq_prefix_suggest_splits(const cvq_shape* s, int q_dtype, int sm_count) {
   if (cvq_partials_bytes(s, 1) == 0 || sm_count < 1 || !is_dtype(q_dtype)) return 1;
   const long long rows = static_cast<long long>(s->batch) * (s->n_q_heads / s->n_kv_heads);
+  if (prefix_on_tensor_cores(s, q_dtype)) {
+    // one CTA per SM; a split holds a tile of each CTA
+    const long long ctas = static_cast<long long>(s->n_kv_heads) * ((rows + 127) / 128) * prefix_pair(s);
+    const long long most = (static_cast<long long>(s->t_cap) + 64 * prefix_pair(s) - 1) / (64 * prefix_pair(s));
+    return static_cast<int>(std::max(1LL, std::min({4096LL, most, sm_count / ctas})));
+  }
   const long long units = s->n_kv_heads * (rows <= 16 ? 1 : (rows + 63) / 64);
   const long long tiles = std::max(1LL, (static_cast<long long>(s->t_cap) + 63) / 64);
   return static_cast<int>(std::max(1LL, std::min({4096LL, tiles, 2LL * sm_count / units})));
@@ -125,8 +138,9 @@ cvq_status cvq_prefix_attend(const cvq_shape* s, const void* q, int q_dtype, con
   a.n_q_heads = s->n_q_heads;
   a.n_kv_heads = s->n_kv_heads;
   a.group = s->n_q_heads / s->n_kv_heads;
+  const bool tensor = prefix_on_tensor_cores(s, q_dtype);
   a.n_splits = n_splits;
-  a.split_tokens = split_tokens_host(s->t_cap, n_splits);
+  a.n_parts = tensor ? n_splits * prefix_pair(s) : n_splits;
   a.lens = prefix_len;
   a.t_cap = s->t_cap;
   a.out = out;
@@ -145,7 +159,7 @@ cvq_status cvq_prefix_attend(const cvq_shape* s, const void* q, int q_dtype, con
   place_workspace(a, workspace);
   if (fault_word_address(&a.fault) != cudaSuccess) return CVQ_ERR_CUDA;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  CVQ_TRY(from_cuda(launch_prefix_f32(a, st)));
+  CVQ_TRY(from_cuda(tensor ? launch_prefix_mma(a, st) : launch_prefix_f32(a, st)));
   return from_cuda(launch_merge(a, st));
 }
 
@@ -254,7 +268,7 @@ cvq_status cvq_paged_attend(const cvq_paged* p, const void* q, int q_dtype, cons
   a.n_q_heads = p->n_q_heads;
   a.n_kv_heads = p->n_kv_heads;
   a.group = p->n_q_heads / p->n_kv_heads;
-  a.n_splits = n_splits;
+  a.n_splits = a.n_parts = n_splits;
   a.t_cap = p->max_pages * p->page_size;
   a.split_tokens = split_tokens_host(a.t_cap, n_splits);
   a.lens = seq_lens;

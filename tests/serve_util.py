@@ -85,7 +85,8 @@ def paged_reference(q, k_pages, v_pages, table, lens, prev=None):
     return merge((out, lse), prev) if prev is not None else (out, lse)
 
 
-def state_tolerance(q, k, v, out, lse, score_err=0.0, v_err=0.0, p_err=0.0, seen_codes=0):
+def state_tolerance(q, k, v, out, lse, score_err=0.0, v_err=0.0, p_err=0.0, seen_codes=0,
+                    v_sq=None):
     """Six standard deviations of (out, lse) errors of rows q [rows, 128] over k, v [T, 128]
     when products of a score carry independent relative errors of at most score_err (each uniform:
     rms = bound / sqrt 3), values v_err and weights p_err, plus fp32 sums.  seen_codes: errors
@@ -93,6 +94,7 @@ def state_tolerance(q, k, v, out, lse, score_err=0.0, v_err=0.0, p_err=0.0, seen
     stops at about that many independent ones."""
     if len(k) == 0:
         return np.full(out.shape, 1e-30), np.full(lse.shape, 1e-30)
+    v_sq = v ** 2 if v_sq is None else v_sq            # what v_err is relative to
     s = q @ k.T / np.sqrt(D)
     p = np.exp(s - lse[:, None])
     rms = np.sqrt((q ** 2) @ (k ** 2).T / D)                       # of a score's products
@@ -101,7 +103,7 @@ def state_tolerance(q, k, v, out, lse, score_err=0.0, v_err=0.0, p_err=0.0, seen
     w = p ** 2 + share * p                                         # weight of independent errors
     dev2 = np.einsum("rt,td->rd", w * (ds2 + p_err ** 2 / 3), v ** 2) \
         + (w * (ds2 + p_err ** 2 / 3)).sum(-1)[:, None] * out ** 2 \
-        + np.einsum("rt,td->rd", w, v ** 2) * (v_err ** 2 / 3)
+        + np.einsum("rt,td->rd", w, v_sq) * (v_err ** 2 / 3)
     rms_v = np.sqrt(p @ v ** 2)
     tol_o = 6 * np.sqrt(dev2) + 2.0 ** -19 * rms_v
     # the sum of weights is kept in fp32; p_err does not enter it
