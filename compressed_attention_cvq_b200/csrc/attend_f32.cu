@@ -74,6 +74,7 @@ __global__ void __launch_bounds__(kThreads) attend_f32_kernel(const __grid_const
   float* sp = sk;                                   // [kTile][RB], over the keys once they are read
   __shared__ unsigned long long f_tab[kPairs];
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");         // the merge
   const int split = blockIdx.x, h = blockIdx.y;
   const int rows = a.batch * a.group;
   const int r0 = blockIdx.z * RB;
@@ -214,28 +215,32 @@ __global__ void __launch_bounds__(kThreads) attend_f32_kernel(const __grid_const
   }
 }
 
-// Merge of the partial states of a row (m in log2 units): one warp per (sequence, query head),
-// 4 dims a lane, U states in flight.
+// Merge of the partial states of a row (m in log2 units): a CTA per (sequence, query head), the
+// states strided over its warps, 4 dims a lane and U states in flight; the warps' sums are joined
+// in their order.  It is launched while the attention kernel still runs and waits for its end.
 constexpr int kMergeWarps = 4;
 __global__ void __launch_bounds__(32 * kMergeWarps) merge_kernel(const __grid_constant__ ServeArgs a) {
-  const size_t row = static_cast<size_t>(blockIdx.x) * kMergeWarps + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  if (row >= static_cast<size_t>(a.batch) * a.n_q_heads) return;
+  __shared__ float s_m[kMergeWarps], s_l[kMergeWarps];
+  __shared__ float4 s_o[kMergeWarps][32];
+  const size_t row = blockIdx.x;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const float* pm = a.part_m + row * a.n_parts;
   const float* pl = a.part_l + row * a.n_parts;
   const float4* po = reinterpret_cast<const float4*>(a.part_o + row * a.n_parts * kHeadDim) + lane;
   constexpr int U = 8;
   float M = -INFINITY, L = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s0 = 0; s0 < a.n_parts; s0 += U) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  for (int s0 = warp; s0 < a.n_parts; s0 += U * kMergeWarps) {
     float mv[U], lv[U];
     float4 x[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const bool in = s0 + u < a.n_parts;
-      mv[u] = in ? pm[s0 + u] : -INFINITY;
-      lv[u] = in ? pl[s0 + u] : 0.f;
-      x[u] = in ? po[static_cast<size_t>(s0 + u) * (kHeadDim / 4)] : make_float4(0.f, 0.f, 0.f, 0.f);
+      const int s = s0 + u * kMergeWarps;
+      const bool in = s < a.n_parts;
+      mv[u] = in ? __ldcg(pm + s) : -INFINITY;
+      lv[u] = in ? __ldcg(pl + s) : 0.f;
+      x[u] = in ? __ldcg(po + static_cast<size_t>(s) * (kHeadDim / 4)) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
     float mn = M;
 #pragma unroll
@@ -251,6 +256,25 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_kernel(const __grid_co
       L = fmaf(lv[u], f, L);
       acc = make_float4(fmaf(x[u].x, f, acc.x), fmaf(x[u].y, f, acc.y), fmaf(x[u].z, f, acc.z), fmaf(x[u].w, f, acc.w));
     }
+  }
+  s_o[warp][lane] = acc;
+  if (lane == 0) {
+    s_m[warp] = M;
+    s_l[warp] = L;
+  }
+  __syncthreads();
+  if (warp != 0) return;
+#pragma unroll
+  for (int w = 1; w < kMergeWarps; ++w) M = fmaxf(M, s_m[w]);
+  L = 0.f;
+  acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int w = 0; w < kMergeWarps; ++w) {
+    if (s_m[w] == -INFINITY && s_l[w] == 0.f) continue;
+    const float f = exp2f(s_m[w] - M);
+    const float4 x = s_o[w][lane];
+    L = fmaf(s_l[w], f, L);
+    acc = make_float4(fmaf(x.x, f, acc.x), fmaf(x.y, f, acc.y), fmaf(x.z, f, acc.z), fmaf(x.w, f, acc.w));
   }
   const float4 y = L == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(acc.x / L, acc.y / L, acc.z / L, acc.w / L);
   store_four(a.out, a.out_dtype, row * kHeadDim + 4 * lane, y);
@@ -277,9 +301,16 @@ cudaError_t launch_prefix_f32(const ServeArgs& a, cudaStream_t stream) {
 }
 
 cudaError_t launch_merge(const ServeArgs& a, cudaStream_t stream) {
-  const size_t rows = static_cast<size_t>(a.batch) * a.n_q_heads;
-  merge_kernel<<<static_cast<unsigned>((rows + kMergeWarps - 1) / kMergeWarps), 32 * kMergeWarps, 0, stream>>>(a);
-  return cudaGetLastError();
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.batch) * a.n_q_heads);
+  cfg.blockDim = dim3(32 * kMergeWarps);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, merge_kernel, a);
 }
 
 }  // namespace cvq

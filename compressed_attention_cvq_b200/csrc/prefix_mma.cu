@@ -6,6 +6,7 @@
 // tokens, in tiles of 64:
 //   producers (8 warps)  gather codewords from fp16 codebooks in shared memory, sum the
 //                        rounds, rotate the keys and store key and value tiles
+//   one thread           copies the codes of four steps ahead into shared memory (8-scalar groups)
 //   one thread           S = Q K^T (M = 128 rows, N = 64 tokens; Q from TMEM), O += P V
 //                        (N = 128 dims; P from TMEM), both tcgen05.mma kind::f16
 //   softmax (2 x 4 warps)  a thread owns a row: even tiles go to the first four warps, odd
@@ -39,11 +40,13 @@ namespace {
 constexpr int kSoftWarps = 8;
 constexpr int kProdWarps = 8;
 constexpr int kProd = 32 * kProdWarps;
-constexpr int kThreads = 32 * (kSoftWarps + kProdWarps + 1);
+constexpr int kMmaWarp = kSoftWarps + kProdWarps, kCopyWarp = kMmaWarp + 1;
+constexpr int kThreads = 32 * (kCopyWarp + 1);
 constexpr int kRows = 128;
 constexpr int kTok = 64;                          // tokens of a tile
 constexpr int kHalfTile = kTok * 128;             // 64 dims of its keys or values, bytes
 constexpr int kTile = 2 * kHalfTile;
+constexpr int kCodeStages = 4;
 constexpr int kReanchor = 64;                     // tiles between exact phases
 constexpr int kOutPitch = kHeadDim + 4;           // floats; 16-byte chunks of 8 rows in 8 bank groups
 constexpr int kOutBytes = kRows * kOutPitch * 4;
@@ -51,6 +54,7 @@ constexpr int kOutBytes = kRows * kOutPitch * 4;
 constexpr uint32_t kColS = 0, kColP = 128, kColQ = 192, kColO = 256, kTmemCols = 512;
 
 struct Control {
+  uint64_t c_full[4], c_empty[4];                 // codes
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], pv_done[2];
   uint32_t tmem;
   alignas(8) uint32_t peak[2][2];                 // [CTA of the pair][keys, values], bits of |x|
@@ -62,19 +66,21 @@ struct Control {
 __device__ __forceinline__ bool wait(uint64_t* bar, unsigned parity, unsigned int* fault) {
   const uint32_t addr = smem_u32(bar);
   unsigned long long t0 = 0;
-  for (int i = 0;; ++i) {
+  for (unsigned i = 1;; ++i) {
     uint32_t done;
     asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n"
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
         " selp.u32 %0, 1, 0, p;\n}"
-        : "=r"(done) : "r"(addr), "r"(parity), "r"(kMbarSuspendHintNs) : "memory");
+        : "=r"(done) : "r"(addr), "r"(parity) : "memory");
     if (done) return true;
-    unsigned long long now;
-    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
-    if (i == 0) t0 = now;
-    else if (now - t0 > kMbarWaitLimitNs) {
-      atomicOr(fault, kFaultCopyTimeout);
-      return false;
+    if (i % 64 == 0) {                            // the clock is slow to read: now and then
+      unsigned long long now;
+      asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
+      if (t0 == 0) t0 = now;
+      else if (now - t0 > kMbarWaitLimitNs) {
+        atomicOr(fault, kFaultCopyTimeout);
+        return false;
+      }
     }
   }
 }
@@ -245,24 +251,38 @@ __device__ __forceinline__ uint32_t stage_codebook(const float* cb, uint32_t dst
   constexpr int CH = 16 / C;                      // chunks of 8 dims that this CTA holds
   const int n = kWide ? R * kWideCodes * 8 : R * kCodes * CH;
   uint32_t peak = 0;
-#pragma unroll 4
-  for (int i = threadIdx.x; i < n; i += kThreads) {
-    const float* src;
-    if (kWide) {
-      src = cb + (static_cast<size_t>(rank) * R * kWideCodes * 8 + i) * 8;
-    } else {
-      const int chunk = i % CH + (C == 2 ? 8 * rank : 0), e = i / CH;      // e = round * 256 + code
-      src = cb + (static_cast<size_t>(chunk) * R * kCodes + e) * 8;
-    }
-    const float4 x = __ldg(reinterpret_cast<const float4*>(src)), y = __ldg(reinterpret_cast<const float4*>(src) + 1);
-    const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+  constexpr int U = 4;                            // 8 loads in flight a thread
+  for (int i0 = threadIdx.x; i0 < n; i0 += U * kThreads) {
+    float4 x[U][2];
 #pragma unroll
-    for (int d = 0; d < 8; ++d) {
-      const uint32_t bits = __float_as_uint(v[d]) & 0x7fffffffu;
-      if (bits < 0x7f800000u) peak = max(peak, bits);
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * kThreads;
+      x[u][0] = x[u][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i < n) {
+        const float* src;
+        if (kWide) {
+          src = cb + (static_cast<size_t>(rank) * R * kWideCodes * 8 + i) * 8;
+        } else {
+          const int chunk = i % CH + (C == 2 ? 8 * rank : 0), e = i / CH;  // e = round * 256 + code
+          src = cb + (static_cast<size_t>(chunk) * R * kCodes + e) * 8;
+        }
+        x[u][0] = __ldg(reinterpret_cast<const float4*>(src));
+        x[u][1] = __ldg(reinterpret_cast<const float4*>(src) + 1);
+      }
     }
-    sts16(dst + i * 16, make_uint4(half_pair(v[0] * scale, v[1] * scale), half_pair(v[2] * scale, v[3] * scale),
-                                   half_pair(v[4] * scale, v[5] * scale), half_pair(v[6] * scale, v[7] * scale)));
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * kThreads;
+      const float v[8] = {x[u][0].x, x[u][0].y, x[u][0].z, x[u][0].w, x[u][1].x, x[u][1].y, x[u][1].z, x[u][1].w};
+#pragma unroll
+      for (int d = 0; d < 8; ++d) {
+        const uint32_t bits = __float_as_uint(v[d]) & 0x7fffffffu;
+        if (bits < 0x7f800000u) peak = max(peak, bits);
+      }
+      if (i < n)
+        sts16(dst + i * 16, make_uint4(half_pair(v[0] * scale, v[1] * scale), half_pair(v[2] * scale, v[3] * scale),
+                                       half_pair(v[4] * scale, v[5] * scale), half_pair(v[6] * scale, v[7] * scale)));
+    }
   }
   return peak;
 }
@@ -296,7 +316,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_mma_kernel(const __grid_co
   const int rounds = kWide ? a.R : R;
   const uint32_t cb_bytes = kWide ? rounds * kWideCodes * 128 : R * kCodes * CH * 16;
   const uint32_t cb_v = cb_k + cb_bytes;
-  const uint32_t ctl_at = max(cb_v + cb_bytes - tiles_k, static_cast<uint32_t>(kOutBytes));
+  // a stage of codes: keys, then values, [token][round][16 groups] as in the cache
+  constexpr uint32_t kCodeBytes = kWide ? 0 : kGroupTok * R * kGroups;
+  const uint32_t ring = cb_v + cb_bytes;
+  const uint32_t ctl_at = max(ring + kCodeStages * 2 * kCodeBytes - tiles_k, static_cast<uint32_t>(kOutBytes));
   Control& ctl = *reinterpret_cast<Control*>(smem + ctl_at);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -324,9 +347,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_mma_kernel(const __grid_co
     return;
   }
 
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");         // the merge
+
   // ---- set-up ----
   if (C == 2) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
-  if (warp == kSoftWarps + kProdWarps) {
+  if (warp == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&ctl.tmem)), "r"(kTmemCols) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     if (lane == 0) {
@@ -339,6 +364,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_mma_kernel(const __grid_co
         mbar_init(&ctl.s_full[s], 1);
         mbar_init(&ctl.p_full[s], nact);
         mbar_init(&ctl.pv_done[s], 1);
+      }
+#pragma unroll
+      for (int s = 0; s < kCodeStages; ++s) {
+        mbar_init(&ctl.c_full[s], 1);
+        mbar_init(&ctl.c_empty[s], kProdWarps);
       }
     }
   }
@@ -532,13 +562,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_mma_kernel(const __grid_co
     step.set(a.phase, chunk, kWide ? 1 : kSlots);
     if (kWide) jump.set(a.phase, chunk, kGroupTok - 3);
     const uint32_t my_k = cb_k + cl * 16, my_v = cb_v + cl * 16;
-    // codes of a step: one byte per (token, round), or a word of 4 tokens per round
-    constexpr int kWords = kWide ? R : 4 * R;
+    // 64-scalar groups: a word with the codes of 4 tokens per round, loaded a step ahead
+    constexpr int kWords = kWide ? R : 1;
     uint32_t wk[kWords], wv[kWords];
     auto load_codes = [&](const uint8_t* codes, uint32_t (&w)[kWords], int i) {
-      const long long t0 = start + static_cast<long long>(i) * kGroupTok;
       if constexpr (kWide) {
-        const long long t = t0 + 4 * slot;
+        const long long t = start + static_cast<long long>(i) * kGroupTok + 4 * slot;
         const size_t row_bytes = a.code_bits == 6 ? static_cast<size_t>(a.t_cap) / 4 * 3 : static_cast<size_t>(a.t_cap);
         const uint8_t* p = codes + (static_cast<size_t>(h) * kWideGroups + rank) * rounds * row_bytes +
                            (a.code_bits == 6 ? t / 4 * 3 : t);
@@ -557,15 +586,15 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_mma_kernel(const __grid_co
             w[r] = 0u;
           }
         }
-      } else {
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const long long t = min(t0 + token(u), end - 1);
-          const uint8_t* p = codes + ((static_cast<size_t>(h) * a.t_cap + t) * R) * kGroups + chunk;
-#pragma unroll
-          for (int r = 0; r < R; ++r) w[u * R + r] = __ldg(p + r * kGroups);
-        }
       }
+    };
+    // 8-scalar groups: codes from the ring (behind the last token any byte, all of them entries)
+    const uint32_t my_codes = ring + token(0) * (R * kGroups) + chunk;
+    auto code = [&](int i, uint32_t values, int u, int r) {
+      uint32_t x;
+      asm volatile("ld.shared.u8 %0, [%1];" : "=r"(x)
+                   : "r"(my_codes + (i % kCodeStages) * (2 * kCodeBytes) + values + u * (kSlots * R * kGroups) + r * kGroups));
+      return x;
     };
     // offset of the codeword of word w and token u within a round of a codebook
     const int unit = a.code_bits == 6 ? 6 : 8;
@@ -596,9 +625,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_mma_kernel(const __grid_co
           else ph.turn(jump);
         }
       } else {
+        if (!wait(&ctl.c_full[i % kCodeStages], (i / kCodeStages) & 1, a.fault)) return false;
+        uint32_t w[4 * R];
+#pragma unroll
+        for (int j = 0; j < 4 * R; ++j) w[j] = code(i, 0, j / R, j % R);
         uint4 v[4 * R];
 #pragma unroll
-        for (int j = 0; j < 4 * R; ++j) v[j] = lds16(my_k + (j % R) * (kCodes * CH * 16) + wk[j] * (CH * 16));
+        for (int j = 0; j < 4 * R; ++j) v[j] = lds16(my_k + (j % R) * (kCodes * CH * 16) + w[j] * (CH * 16));
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           float x[8];
@@ -638,12 +671,18 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_mma_kernel(const __grid_co
                                   half_pair(x[k][6], x[k][7]));
         }
       } else {
+        uint32_t w[4 * R];
+#pragma unroll
+        for (int j = 0; j < 4 * R; ++j) w[j] = code(i, kCodeBytes, j / R, j % R);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) v[u] = lds16(my_v + w[u * R] * (CH * 16));
+        __syncwarp();
+        if (lane == 0) arrive(&ctl.c_empty[i % kCodeStages]);
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          v[u] = lds16(my_v + wv[u * R] * (CH * 16));
 #pragma unroll
           for (int r = 1; r < R; ++r) {
-            const uint4 y = lds16(my_v + r * (kCodes * CH * 16) + wv[u * R + r] * (CH * 16));
+            const uint4 y = lds16(my_v + r * (kCodes * CH * 16) + w[u * R + r] * (CH * 16));
             v[u] = make_uint4(add_halves(v[u].x, y.x), add_halves(v[u].y, y.y), add_halves(v[u].z, y.z), add_halves(v[u].w, y.w));
           }
         }
@@ -663,6 +702,27 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_mma_kernel(const __grid_co
     for (int i = 0; ok && i < ntiles; ++i) {
       if (i + 1 < ntiles) ok = make_keys(i + 1);
       ok = ok && make_values(i);
+    }
+  } else if (warp == kCopyWarp) {
+    // ================= codes =================
+    if constexpr (!kWide) {
+      const size_t row = static_cast<size_t>(R) * kGroups;
+      if (lane == 0) {
+        for (int i = 0; i < ntiles; ++i) {
+          const int s = i % kCodeStages;
+          if (i >= kCodeStages && !wait(&ctl.c_empty[s], (i / kCodeStages - 1) & 1, a.fault)) break;
+          const long long t = start + static_cast<long long>(i) * kGroupTok;
+          const uint32_t bytes = static_cast<uint32_t>(min(end - t, static_cast<long long>(kGroupTok))) * static_cast<uint32_t>(row);
+          const size_t at = (static_cast<size_t>(h) * a.t_cap + t) * row;
+          unsigned char* dst = smem + (ring - tiles_k) + s * (2 * kCodeBytes);
+          mbar_expect_tx(&ctl.c_full[s], 2 * bytes);
+          bulk_load(dst, a.key_codes + at, bytes, &ctl.c_full[s]);
+          bulk_load(dst + kCodeBytes, a.val_codes + at, bytes, &ctl.c_full[s]);
+        }
+        // no copy is left in flight, whatever ended the others' loops
+        for (int i = max(0, ntiles - kCodeStages); i < ntiles; ++i)
+          if (!wait(&ctl.c_full[i % kCodeStages], (i / kCodeStages) & 1, a.fault)) break;
+      }
     }
   } else if (lane == 0) {
     // ================= matrix products =================
@@ -755,7 +815,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_mma_kernel(const __grid_co
     *reinterpret_cast<float4*>(a.part_o + (global_row(rr) * n_parts + blockIdx.x) * kHeadDim + c) =
         *reinterpret_cast<const float4*>(rows_out + rr * kOutPitch + c);
   }
-  if (warp == kSoftWarps + kProdWarps)
+  if (warp == kMmaWarp)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
   if (C == 2) cluster_barrier();                  // the other CTA may still store here until now
 }
@@ -764,11 +824,12 @@ template <int C, bool kWide, int R>
 cudaError_t run(const ServeArgs& a, cudaStream_t stream) {
   static PerDeviceFlag flag;
   constexpr int kTiles = (kWide ? 3 : 4) * kTile;
-  constexpr size_t kMost = kTiles + (kWide ? 2u * R * kWideCodes * 128 : 2u * R * kCodes * (16 / C) * 16) + sizeof(Control);
+  constexpr size_t kCodes8 = kWide ? 0 : kCodeStages * 2 * C * kTok * R * kGroups;
+  constexpr size_t kMost = kTiles + (kWide ? 2u * R * kWideCodes * 128 : 2u * R * kCodes * (16 / C) * 16) + kCodes8 + sizeof(Control);
   static_assert(kMost <= 227 * 1024, "fits an SM");
   cudaError_t e = set_smem_limit_once(flag, prefix_mma_kernel<C, kWide, R>, kMost);
   if (e != cudaSuccess) return e;
-  size_t bytes = kTiles + (kWide ? 2u * a.R * kWideCodes * 128 : 2u * R * kCodes * (16 / C) * 16);
+  size_t bytes = kTiles + (kWide ? 2u * a.R * kWideCodes * 128 : 2u * R * kCodes * (16 / C) * 16) + kCodes8;
   if (bytes < kOutBytes) bytes = kOutBytes;
   bytes += sizeof(Control);
   cudaLaunchAttribute attr[1];
