@@ -54,11 +54,11 @@ constexpr int kOutBytes = kRows * kOutPitch * 4;
 constexpr uint32_t kColS = 0, kColP = 128, kColQ = 192, kColO = 256, kTmemCols = 512;
 
 struct Control {
-  uint64_t c_full[4], c_empty[4];                 // codes
+  uint64_t book;                                  // codebooks
+  uint64_t q_full;
+  uint64_t c_full[kCodeStages], c_empty[kCodeStages];                       // codes
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], pv_done[2];
   uint32_t tmem;
-  alignas(8) uint32_t peak[2][2];                 // [CTA of the pair][keys, values], bits of |x|
-  uint32_t warp_peak[2][kThreads / 32];
   float m[kRows], l[kRows];                       // second stream's state
 };
 
@@ -91,9 +91,6 @@ __device__ __forceinline__ uint32_t map_to(uint32_t addr, uint32_t rank) {
   uint32_t r;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
   return r;
-}
-__device__ __forceinline__ void arrive_at(uint64_t* bar, uint32_t rank) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(map_to(smem_u32(bar), rank)) : "memory");
 }
 __device__ __forceinline__ void cluster_barrier() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -146,8 +143,15 @@ __device__ __forceinline__ uint4 lds16(uint32_t addr) {
 __device__ __forceinline__ void sts16(uint32_t addr, uint4 v) {
   asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
-__device__ __forceinline__ void sts16_cluster(uint32_t addr, uint4 v) {
-  asm volatile("st.shared::cluster.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+// to the other CTA; its barrier counts the bytes as they land, so that nothing waits for them here
+__device__ __forceinline__ void send16(uint32_t addr, uint4 v, uint32_t bar) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%1,%2,%3,%4}, [%5];" ::"r"(addr), "r"(v.x),
+               "r"(v.y), "r"(v.z), "r"(v.w), "r"(bar) : "memory");
+}
+__device__ __forceinline__ bool elect_one() {
+  uint32_t yes;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(yes));
+  return yes != 0;
 }
 // pairs of fp32 numbers in one instruction
 using f2 = unsigned long long;
@@ -243,53 +247,62 @@ struct Phase {
   }
 };
 
-// ---- codebooks to shared memory ----
-// One CTA's share of a KV head's codebook as fp16 times `scale`; returns the bits of the
-// largest finite |x| that this thread saw.
+// ---- codebooks ----
+// A CTA holds chunk (of 8 dims) * entry items of 16 bytes: i -> [round][entry][chunk] of its CH
+// chunks, which for a 64-scalar group is the codebook's own order.
 template <int C, bool kWide>
-__device__ __forceinline__ uint32_t stage_codebook(const float* cb, uint32_t dst, int R, int rank, float scale) {
-  constexpr int CH = 16 / C;                      // chunks of 8 dims that this CTA holds
-  const int n = kWide ? R * kWideCodes * 8 : R * kCodes * CH;
-  uint32_t peak = 0;
-  constexpr int U = 4;                            // 8 loads in flight a thread
-  for (int i0 = threadIdx.x; i0 < n; i0 += U * kThreads) {
-    float4 x[U][2];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int i = i0 + u * kThreads;
-      x[u][0] = x[u][1] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (i < n) {
-        const float* src;
-        if (kWide) {
-          src = cb + (static_cast<size_t>(rank) * R * kWideCodes * 8 + i) * 8;
-        } else {
-          const int chunk = i % CH + (C == 2 ? 8 * rank : 0), e = i / CH;  // e = round * 256 + code
-          src = cb + (static_cast<size_t>(chunk) * R * kCodes + e) * 8;
-        }
-        x[u][0] = __ldg(reinterpret_cast<const float4*>(src));
-        x[u][1] = __ldg(reinterpret_cast<const float4*>(src) + 1);
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int i = i0 + u * kThreads;
-      const float v[8] = {x[u][0].x, x[u][0].y, x[u][0].z, x[u][0].w, x[u][1].x, x[u][1].y, x[u][1].z, x[u][1].w};
-#pragma unroll
-      for (int d = 0; d < 8; ++d) {
-        const uint32_t bits = __float_as_uint(v[d]) & 0x7fffffffu;
-        if (bits < 0x7f800000u) peak = max(peak, bits);
-      }
-      if (i < n)
-        sts16(dst + i * 16, make_uint4(half_pair(v[0] * scale, v[1] * scale), half_pair(v[2] * scale, v[3] * scale),
-                                       half_pair(v[4] * scale, v[5] * scale), half_pair(v[6] * scale, v[7] * scale)));
-    }
-  }
-  return peak;
+__device__ __forceinline__ const float* book_item(const float* cb, int R, int rank, int i) {
+  constexpr int CH = 16 / C;
+  if (kWide) return cb + (static_cast<size_t>(rank) * R * kWideCodes * 8 + i) * 8;
+  const int chunk = i % CH + (C == 2 ? 8 * rank : 0);
+  return cb + (static_cast<size_t>(chunk) * R * kCodes + i / CH) * 8;
+}
+template <int C, bool kWide>
+__host__ __device__ constexpr int book_items(int R) {
+  return kWide ? R * kWideCodes * 8 : R * kCodes * (16 / C);
+}
+__device__ __forceinline__ uint4 scaled_halves(float4 x, float4 y, float scale) {
+  return make_uint4(half_pair(x.x * scale, x.y * scale), half_pair(x.z * scale, x.w * scale),
+                    half_pair(y.x * scale, y.y * scale), half_pair(y.z * scale, y.w * scale));
 }
 
 // Exponent of the codebook scale: 6 wherever the decoded numbers then lie well inside fp16's
 // range, so that one reading of the codebook is enough; else what takes the largest to 2^14.
 constexpr int kUsualScale = 6;
+constexpr int kBookThreads = 256;
+
+// The codebooks as CTAs of the attention kernel hold them, in fp16 times 2^kUsualScale, into
+// the workspace, and the largest finite |x| of every 256 items: converted once a call, and read
+// from there by all the CTAs of a KV head in half the bytes.  Launched before the attention
+// kernel, whose own set-up runs under it.
+template <int C, bool kWide>
+__global__ void __launch_bounds__(kBookThreads) prefix_book_kernel(const __grid_constant__ ServeArgs a) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  __shared__ uint32_t warp_peak[kBookThreads / 32];
+  const int n = book_items<C, kWide>(a.R), i = blockIdx.x * kBookThreads + threadIdx.x;
+  const int rank = blockIdx.y >> 1, values = blockIdx.y & 1, h = blockIdx.z;
+  const float* cb = values ? a.val_cb + static_cast<long long>(h) * a.val_cb_stride
+                           : a.key_cb + static_cast<long long>(h) * a.key_cb_stride;
+  const float* src = book_item<C, kWide>(cb, a.R, rank, i);
+  const float4 x = __ldg(reinterpret_cast<const float4*>(src)), y = __ldg(reinterpret_cast<const float4*>(src) + 1);
+  const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+  uint32_t peak = 0;
+#pragma unroll
+  for (int d = 0; d < 8; ++d) {
+    const uint32_t bits = __float_as_uint(v[d]) & 0x7fffffffu;
+    if (bits < 0x7f800000u) peak = max(peak, bits);
+  }
+  reinterpret_cast<uint4*>(a.book)[((static_cast<size_t>(h) * C + rank) * 2 + values) * n + i] =
+      scaled_halves(x, y, static_cast<float>(1 << kUsualScale));
+  peak = __reduce_max_sync(0xffffffffu, peak);
+  if ((threadIdx.x & 31) == 0) warp_peak[threadIdx.x >> 5] = peak;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+#pragma unroll
+    for (int w = 1; w < kBookThreads / 32; ++w) peak = max(peak, warp_peak[w]);
+    a.book_peak[((static_cast<size_t>(h) * 2 + values) * C + rank) * gridDim.x + blockIdx.x] = peak;
+  }
+}
 __device__ __forceinline__ int scale_exponent(uint32_t peak_bits, int R) {
   const float most = __uint_as_float(peak_bits) * static_cast<float>(R) * 1.5f;      // 1.5 > sqrt 2: rotated
   if (peak_bits == 0 || (most < 512.f && most > 0.0078125f)) return kUsualScale;
@@ -339,6 +352,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_mma_kernel(const __grid_co
   const long long start = min(per * split, static_cast<long long>(L)), end = min(start + per, static_cast<long long>(L));
   const int ntiles = static_cast<int>((end - start + kGroupTok - 1) / kGroupTok);
   if (ntiles == 0) {                              // the same for both CTAs of a pair
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (threadIdx.x < nrows) {
       const size_t at = global_row(threadIdx.x) * n_parts + blockIdx.x;
       a.part_m[at] = -INFINITY;
@@ -347,109 +361,46 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_mma_kernel(const __grid_co
     return;
   }
 
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");         // the merge
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");          // the merge
 
   // ---- set-up ----
-  if (C == 2) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   if (warp == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&ctl.tmem)), "r"(kTmemCols) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-    if (lane == 0) {
+  } else if (warp == kCopyWarp && lane == 0) {
+    mbar_init(&ctl.book, 1);
+    mbar_init(&ctl.q_full, nact);
 #pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        mbar_init(&ctl.k_full[s], kProdWarps * C);
-        mbar_init(&ctl.v_full[s], kProdWarps * C);
-        mbar_init(&ctl.k_empty[s], C);
-        mbar_init(&ctl.v_empty[s], C);
-        mbar_init(&ctl.s_full[s], 1);
-        mbar_init(&ctl.p_full[s], nact);
-        mbar_init(&ctl.pv_done[s], 1);
-      }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&ctl.k_full[s], kProdWarps);
+      mbar_init(&ctl.v_full[s], kProdWarps);
+      mbar_init(&ctl.k_empty[s], C);
+      mbar_init(&ctl.v_empty[s], C);
+      mbar_init(&ctl.s_full[s], 1);
+      mbar_init(&ctl.p_full[s], nact);
+      mbar_init(&ctl.pv_done[s], 1);
+    }
 #pragma unroll
-      for (int s = 0; s < kCodeStages; ++s) {
-        mbar_init(&ctl.c_full[s], 1);
-        mbar_init(&ctl.c_empty[s], kProdWarps);
-      }
+    for (int s = 0; s < kCodeStages; ++s) {
+      mbar_init(&ctl.c_full[s], 1);
+      mbar_init(&ctl.c_empty[s], kProdWarps);
     }
   }
-  const float* kcb = a.key_cb + static_cast<long long>(h) * a.key_cb_stride;
-  const float* vcb = a.val_cb + static_cast<long long>(h) * a.val_cb_stride;
-  constexpr float kUsual = static_cast<float>(1 << kUsualScale);
-  uint32_t pk = stage_codebook<C, kWide>(kcb, cb_k, rounds, rank, kUsual);
-  uint32_t pv = stage_codebook<C, kWide>(vcb, cb_v, rounds, rank, kUsual);
-  pk = __reduce_max_sync(0xffffffffu, pk);
-  pv = __reduce_max_sync(0xffffffffu, pv);
-  if (lane == 0) {
-    ctl.warp_peak[0][warp] = pk;
-    ctl.warp_peak[1][warp] = pv;
-  }
+  __syncwarp();
   tmem_before_sync();
-  __syncthreads();
+  if (C == 2) cluster_barrier();                  // the other CTA runs, and its barriers are there
+  else __syncthreads();
   tmem_after_sync();
-  pk = __reduce_max_sync(0xffffffffu, lane < kThreads / 32 ? ctl.warp_peak[0][lane] : 0u);
-  pv = __reduce_max_sync(0xffffffffu, lane < kThreads / 32 ? ctl.warp_peak[1][lane] : 0u);
-  if (C == 2) {
-    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");            // the other CTA runs
-    if (threadIdx.x == 0) {
-#pragma unroll
-      for (uint32_t to = 0; to < 2; ++to) {
-        const uint32_t at = map_to(smem_u32(&ctl.peak[rank][0]), to);
-        asm volatile("st.shared::cluster.v2.u32 [%0], {%1,%2};" ::"r"(at), "r"(pk), "r"(pv) : "memory");
-      }
-    }
-    __syncwarp();
-    cluster_barrier();                            // barriers and peaks of both CTAs are there
-    pk = max(ctl.peak[0][0], ctl.peak[1][0]);
-    pv = max(ctl.peak[0][1], ctl.peak[1][1]);
-  }
-  const int ek = scale_exponent(pk, rounds), ev = scale_exponent(pv, rounds);
-  if (ek != kUsualScale) stage_codebook<C, kWide>(kcb, cb_k, rounds, rank, ldexpf(1.f, ek));
-  if (ev != kUsualScale) stage_codebook<C, kWide>(vcb, cb_v, rounds, rank, ldexpf(1.f, ev));
   const uint32_t tmem = ctl.tmem;
-
-  // query rows: scale of each (both streams), and the operand (first stream)
-  float factor = 0.f;
-  if (warp < kSoftWarps && (warp & 3) < nact) {
-    const int r = (warp & 3) * 32 + lane;
-    const bool bf16 = a.q_dtype == CVQ_BF16;
-    const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + global_row(min(r, nrows - 1)) * kHeadDim);
-    float mx = 0.f;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const uint4 v = __ldg(src + i);
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 f = query_pair(w[j], bf16);
-        mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
-      }
-    }
-    // largest element to [2^8, 2^9)
-    const int eq = mx > 0.f && mx < INFINITY ? 8 - ilogbf(mx) : 0;
-    factor = ldexpf(0.08838834764831845f * kLog2e, -eq - ek);
-    if (warp < 4) {
-      const float up = ldexpf(1.f, min(eq, 127)), rest = ldexpf(1.f, eq - min(eq, 127));
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        uint32_t out[32];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint4 v = __ldg(src + half * 8 + i);
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float2 f = query_pair(w[j], bf16);
-            out[4 * i + j] = r < nrows ? half_pair(f.x * up * rest, f.y * up * rest) : 0u;
-          }
-        }
-        tmem_store32(tmem + (static_cast<uint32_t>(warp * 32) << 16) + kColQ + half * 32, out);
-      }
-      tmem_store_wait();
-    }
-  }
-  tmem_before_sync();
-  __syncthreads();
-  tmem_after_sync();
+  // scale exponent of the key (0) or value (1) codebook of this KV head; after the wait for
+  // prefix_book_kernel
+  auto book_exponent = [&](int values) {
+    const int n = C * book_items<C, kWide>(rounds) / kBookThreads;
+    const uint32_t* at = a.book_peak + (static_cast<size_t>(h) * 2 + values) * n;
+    uint32_t peak = 0;
+    for (int i = lane; i < n; i += 32) peak = max(peak, __ldcg(at + i));
+    return scale_exponent(__reduce_max_sync(0xffffffffu, peak), rounds);
+  };
 
   float m = -INFINITY, l = 0.f;                   // softmax: log2 maximum and sum of this thread's row
   if (warp < kSoftWarps) {
@@ -460,6 +411,47 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_mma_kernel(const __grid_co
     // rescaled a few times and not at every tile, and weights stay below 2^(kLift + kSlack)
     constexpr float kLift = 7.f, kSlack = 8.f;
     if (q4 < nact) {
+      // the query row: its scale (both streams), and the operand (first stream)
+      const int r = q4 * 32 + lane;
+      const bool bf16 = a.q_dtype == CVQ_BF16;
+      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + global_row(min(r, nrows - 1)) * kHeadDim);
+      float qmax = 0.f;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const uint4 v = __ldg(src + i);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 f = query_pair(w[j], bf16);
+          qmax = fmaxf(qmax, fmaxf(fabsf(f.x), fabsf(f.y)));
+        }
+      }
+      // largest element to [2^8, 2^9)
+      const int eq = qmax > 0.f && qmax < INFINITY ? 8 - ilogbf(qmax) : 0;
+      if (st == 0) {
+        const float up = ldexpf(1.f, min(eq, 127)), rest = ldexpf(1.f, eq - min(eq, 127));
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t out[32];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const uint4 v = __ldg(src + half * 8 + i);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float2 f = query_pair(w[j], bf16);
+              out[4 * i + j] = r < nrows ? half_pair(f.x * up * rest, f.y * up * rest) : 0u;
+            }
+          }
+          tmem_store32(lanes + kColQ + half * 32, out);
+        }
+        tmem_store_wait();
+        tmem_before_sync();
+        __syncwarp();
+        if (lane == 0) arrive(&ctl.q_full);
+      }
+      asm volatile("griddepcontrol.wait;" ::: "memory");
+      const float factor = ldexpf(0.08838834764831845f * kLog2e, -eq - book_exponent(0));
       for (int i = st; i < ntiles; i += 2) {
         const unsigned par = (i >> 1) & 1;
         if (!wait(&ctl.s_full[st], par, a.fault)) break;
@@ -539,54 +531,56 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_mma_kernel(const __grid_co
       const int row = token(u) % kTok, to = C == 2 ? token(u) / kTok : 0;
       mine[u] = to == rank;
       at[u] = (chunk >> 3) * kHalfTile + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);
-      if (!mine[u]) at[u] = map_to(tiles_k + at[u], static_cast<uint32_t>(to)) - tiles_k;
+      if (!mine[u]) at[u] += C == 2 ? map_to(tiles_k, static_cast<uint32_t>(to)) - tiles_k : 0;
     }
-    auto store = [&](uint32_t tile, int u, uint4 v) {
+    const uint32_t away = C == 2 ? map_to(tiles_k, static_cast<uint32_t>(rank ^ 1)) - tiles_k : 0;
+    auto store = [&](uint32_t tile, int u, uint4 v, uint64_t* bar) {
       if (C == 1 || mine[u]) sts16(tile + at[u], v);
-      else sts16_cluster(tile + at[u], v);
+      else send16(tile + at[u], v, smem_u32(bar) + away);
     };
+    // a stage is full when this CTA's warps have stored and the other CTA's half has landed
     auto publish = [&](uint64_t* bar) {
-      if (C == 2) asm volatile("fence.proxy.async;" ::: "memory");
-      else fence_proxy_async_smem();
+      fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        if (C == 2) {
-          arrive_at(bar, 0);
-          arrive_at(bar, 1);
-        } else {
-          arrive(bar);
-        }
+        if (C == 2 && warp == kSoftWarps) mbar_expect_tx(bar, kHalfTile);
+        else arrive(bar);
       }
     };
     Phase ph, step, jump;
     step.set(a.phase, chunk, kWide ? 1 : kSlots);
     if (kWide) jump.set(a.phase, chunk, kGroupTok - 3);
     const uint32_t my_k = cb_k + cl * 16, my_v = cb_v + cl * 16;
-    // 64-scalar groups: a word with the codes of 4 tokens per round, loaded a step ahead
-    constexpr int kWords = kWide ? R : 1;
-    uint32_t wk[kWords], wv[kWords];
-    auto load_codes = [&](const uint8_t* codes, uint32_t (&w)[kWords], int i) {
+    // 64-scalar groups: a word holds the codes of this slot's 4 tokens for a round; the 8 threads
+    // of a slot load two rounds each, a step ahead, and pass them around
+    static_assert(!kWide || R <= 16, "two rounds a thread");
+    struct Words {
+      uint32_t lo[2], hi[2];
+    };
+    Words raw_k, raw_v;
+    // packed codes: the word is 24 bits from byte t / 4 * 3 of a row, in one or two aligned words;
+    // every row and step has the same alignment (t_cap and steps are multiples of 64 tokens)
+    const unsigned shift = kWide && a.code_bits == 6 ? (3u * slot & 3u) * 8u : 0u;
+    auto load_codes = [&](const uint8_t* codes, Words& w, int i) {
       if constexpr (kWide) {
         const long long t = start + static_cast<long long>(i) * kGroupTok + 4 * slot;
         const size_t row_bytes = a.code_bits == 6 ? static_cast<size_t>(a.t_cap) / 4 * 3 : static_cast<size_t>(a.t_cap);
-        const uint8_t* p = codes + (static_cast<size_t>(h) * kWideGroups + rank) * rounds * row_bytes +
-                           (a.code_bits == 6 ? t / 4 * 3 : t);
-        const bool in = t < end;                  // rows are whole words: t .. t + 3 lie inside
-        // packed: the 24 bits from p, out of one or two aligned words
-        const unsigned shift = a.code_bits == 6 ? (reinterpret_cast<uintptr_t>(p) & 3) * 8 : 0;
+        const uint8_t* p = codes + ((static_cast<size_t>(h) * kWideGroups + rank) * rounds + cl) * row_bytes +
+                           (a.code_bits == 6 ? t / 4 * 3 - (shift >> 3) : t);
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-          if (r < rounds && in) {
-            const uint8_t* q = p + r * row_bytes;
-            // rows of 3 t_cap / 4 bytes, t_cap a multiple of 64: every row has p's alignment
-            const uint32_t* word = reinterpret_cast<const uint32_t*>(q - (shift >> 3));
-            const uint32_t lo = __ldg(word), hi = shift > 8 ? __ldg(word + 1) : 0u;
-            w[r] = __funnelshift_r(lo, hi, shift);
-          } else {
-            w[r] = 0u;
+        for (int k = 0; k < 2; ++k, p += 8 * row_bytes) {
+          w.lo[k] = w.hi[k] = 0u;
+          if (cl + 8 * k < rounds && t < end) {
+            w.lo[k] = __ldg(reinterpret_cast<const uint32_t*>(p));
+            if (shift > 8) w.hi[k] = __ldg(reinterpret_cast<const uint32_t*>(p) + 1);
           }
         }
       }
+    };
+    auto share_codes = [&](const Words& w, uint32_t (&of)[kWide ? R : 1]) {
+      const uint32_t w0 = __funnelshift_r(w.lo[0], w.hi[0], shift), w1 = __funnelshift_r(w.lo[1], w.hi[1], shift);
+#pragma unroll
+      for (int r = 0; r < (kWide ? R : 1); ++r) of[r] = __shfl_sync(0xffffffffu, r < 8 ? w0 : w1, (lane & 24) | (r & 7));
     };
     // 8-scalar groups: codes from the ring (behind the last token any byte, all of them entries)
     const uint32_t my_codes = ring + token(0) * (R * kGroups) + chunk;
@@ -606,6 +600,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_mma_kernel(const __grid_co
       if (i % kReanchor == 0)
         ph.set(a.phase, chunk, static_cast<unsigned long long>(start + static_cast<long long>(i) * kGroupTok + token(0)));
       if constexpr (kWide) {
+        uint32_t wk[R];
+        share_codes(raw_k, wk);
 #pragma unroll
         for (int u = 0; u < 4; u += 2) {
           float x[2][8];
@@ -618,9 +614,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_mma_kernel(const __grid_co
               add_chunk(x[1], lds16(my_k + r * (kWideCodes * 128) + entry(wk[r], u + 1)));
             }
           }
-          store(tile, u, ph.rotate(x[0]));
+          store(tile, u, ph.rotate(x[0]), &ctl.k_full[s]);
           ph.turn(step);
-          store(tile, u + 1, ph.rotate(x[1]));
+          store(tile, u + 1, ph.rotate(x[1]), &ctl.k_full[s]);
           if (u == 0) ph.turn(step);
           else ph.turn(jump);
         }
@@ -638,12 +634,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_mma_kernel(const __grid_co
           set_chunk(x, v[u * R]);
 #pragma unroll
           for (int r = 1; r < R; ++r) add_chunk(x, v[u * R + r]);
-          store(tile, u, ph.rotate(x));
+          store(tile, u, ph.rotate(x), &ctl.k_full[s]);
           ph.turn(step);
         }
       }
       publish(&ctl.k_full[s]);
-      if (i + 1 < ntiles) load_codes(a.key_codes, wk, i + 1);
+      if (i + 1 < ntiles) load_codes(a.key_codes, raw_k, i + 1);
       return true;
     };
     auto make_values = [&](int i) {
@@ -653,6 +649,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_mma_kernel(const __grid_co
       const long long left = end - (start + static_cast<long long>(i) * kGroupTok);
       uint4 v[4];
       if constexpr (kWide) {
+        uint32_t wv[R];
+        share_codes(raw_v, wv);
 #pragma unroll
         for (int u = 0; u < 4; u += 2) {
           float x[2][8];
@@ -690,14 +688,29 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_mma_kernel(const __grid_co
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         if (token(u) >= left) v[u] = make_uint4(0u, 0u, 0u, 0u);            // weight 0 times this must be 0
-        store(tile, u, v[u]);
+        store(tile, u, v[u], &ctl.v_full[s]);
       }
       publish(&ctl.v_full[s]);
-      if (i + 1 < ntiles) load_codes(a.val_codes, wv, i + 1);
+      if (i + 1 < ntiles) load_codes(a.val_codes, raw_v, i + 1);
       return true;
     };
-    load_codes(a.key_codes, wk, 0);
-    load_codes(a.val_codes, wv, 0);
+    load_codes(a.key_codes, raw_k, 0);
+    load_codes(a.val_codes, raw_v, 0);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int ek = book_exponent(0), ev = book_exponent(1);
+    wait(&ctl.book, 0, a.fault);
+    if (ek != kUsualScale || ev != kUsualScale) {
+      // far from the usual size: scaled anew, from the codebooks themselves
+      const float* kcb = a.key_cb + static_cast<long long>(h) * a.key_cb_stride;
+      const float* vcb = a.val_cb + static_cast<long long>(h) * a.val_cb_stride;
+      for (int i = tid; i < book_items<C, kWide>(rounds); i += kProd) {
+        const float4* k = reinterpret_cast<const float4*>(book_item<C, kWide>(kcb, rounds, rank, i));
+        const float4* v = reinterpret_cast<const float4*>(book_item<C, kWide>(vcb, rounds, rank, i));
+        sts16(cb_k + i * 16, scaled_halves(__ldg(k), __ldg(k + 1), ldexpf(1.f, ek)));
+        sts16(cb_v + i * 16, scaled_halves(__ldg(v), __ldg(v + 1), ldexpf(1.f, ev)));
+      }
+      asm volatile("bar.sync 1, %0;" ::"n"(kProd) : "memory");
+    }
     bool ok = make_keys(0);                       // keys run one tile ahead of the values
     for (int i = 0; ok && i < ntiles; ++i) {
       if (i + 1 < ntiles) ok = make_keys(i + 1);
@@ -705,26 +718,38 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_mma_kernel(const __grid_co
     }
   } else if (warp == kCopyWarp) {
     // ================= codes =================
-    if constexpr (!kWide) {
+    if (lane == 0) {
       const size_t row = static_cast<size_t>(R) * kGroups;
-      if (lane == 0) {
-        for (int i = 0; i < ntiles; ++i) {
-          const int s = i % kCodeStages;
-          if (i >= kCodeStages && !wait(&ctl.c_empty[s], (i / kCodeStages - 1) & 1, a.fault)) break;
-          const long long t = start + static_cast<long long>(i) * kGroupTok;
-          const uint32_t bytes = static_cast<uint32_t>(min(end - t, static_cast<long long>(kGroupTok))) * static_cast<uint32_t>(row);
-          const size_t at = (static_cast<size_t>(h) * a.t_cap + t) * row;
-          unsigned char* dst = smem + (ring - tiles_k) + s * (2 * kCodeBytes);
-          mbar_expect_tx(&ctl.c_full[s], 2 * bytes);
-          bulk_load(dst, a.key_codes + at, bytes, &ctl.c_full[s]);
-          bulk_load(dst + kCodeBytes, a.val_codes + at, bytes, &ctl.c_full[s]);
-        }
+      auto copy_codes = [&](int i) {
+        const int s = i % kCodeStages;
+        if (i >= kCodeStages && !wait(&ctl.c_empty[s], (i / kCodeStages - 1) & 1, a.fault)) return false;
+        const long long t = start + static_cast<long long>(i) * kGroupTok;
+        const uint32_t bytes = static_cast<uint32_t>(min(end - t, static_cast<long long>(kGroupTok))) * static_cast<uint32_t>(row);
+        const size_t at = (static_cast<size_t>(h) * a.t_cap + t) * row;
+        unsigned char* dst = smem + (ring - tiles_k) + s * (2 * kCodeBytes);
+        mbar_expect_tx(&ctl.c_full[s], 2 * bytes);
+        bulk_load(dst, a.key_codes + at, bytes, &ctl.c_full[s]);
+        bulk_load(dst + kCodeBytes, a.val_codes + at, bytes, &ctl.c_full[s]);
+        return true;
+      };
+      const int first = kWide ? 0 : min(ntiles, kCodeStages);
+      for (int i = 0; i < first; ++i) copy_codes(i);
+      asm volatile("griddepcontrol.wait;" ::: "memory");
+      constexpr uint32_t kPiece = 16384;
+      mbar_expect_tx(&ctl.book, 2 * cb_bytes);
+      const unsigned char* book = static_cast<const unsigned char*>(a.book) + (static_cast<size_t>(h) * C + rank) * (2 * cb_bytes);
+      for (uint32_t at = 0; at < 2 * cb_bytes; at += kPiece)
+        bulk_load(smem + (cb_k - tiles_k) + at, book + at, min(kPiece, 2 * cb_bytes - at), &ctl.book);
+      if (!kWide) {
+        bool ok = true;
+        for (int i = first; ok && i < ntiles; ++i) ok = copy_codes(i);
         // no copy is left in flight, whatever ended the others' loops
-        for (int i = max(0, ntiles - kCodeStages); i < ntiles; ++i)
-          if (!wait(&ctl.c_full[i % kCodeStages], (i / kCodeStages) & 1, a.fault)) break;
+        for (int i = max(0, ntiles - kCodeStages); ok && i < ntiles; ++i)
+          ok = wait(&ctl.c_full[i % kCodeStages], (i / kCodeStages) & 1, a.fault);
       }
+      wait(&ctl.book, 0, a.fault);
     }
-  } else if (lane == 0) {
+  } else {
     // ================= matrix products =================
     // A tile is two halves of 64 dims, each [64 tokens][128 bytes] with 16-byte chunk c of row t
     // at c ^ (t & 7).  As keys (N = tokens, K = dims, K-major) 8 rows are 1024 bytes apart and 16
@@ -732,18 +757,22 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_mma_kernel(const __grid_co
     // tokens 1024 bytes.
     constexpr uint32_t kDescS = (1u << 4) | ((kTok >> 3) << 17) | ((kRows >> 4) << 24);
     constexpr uint32_t kDescO = (1u << 4) | (1u << 16) | ((kHeadDim >> 3) << 17) | ((kRows >> 4) << 24);
-    for (int i = 0; i <= ntiles; ++i) {
+    bool ok = wait(&ctl.q_full, 0, a.fault);
+    for (int i = 0; ok && i <= ntiles; ++i) {
       if (i < ntiles) {
         const int s = i & 1;
         if (!wait(&ctl.k_full[s], (i >> 1) & 1, a.fault)) break;
         asm volatile("fence.proxy.async;" ::: "memory");
         tmem_after_sync();
+        if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          mma_f16(tmem + kColS + s * kTok, tmem + kColQ + 8 * k,
-                  operand(tiles_k + s * kTile + (k >> 2) * kHalfTile + (k & 3) * 32, 16, 1024), kDescS, k > 0);
-        commit<C>(&ctl.s_full[s], false);
-        if (i + 2 < ntiles) commit<C>(&ctl.k_empty[s], true);
+          for (int k = 0; k < 8; ++k)
+            mma_f16(tmem + kColS + s * kTok, tmem + kColQ + 8 * k,
+                    operand(tiles_k + s * kTile + (k >> 2) * kHalfTile + (k & 3) * 32, 16, 1024), kDescS, k > 0);
+          commit<C>(&ctl.s_full[s], false);
+          if (i + 2 < ntiles) commit<C>(&ctl.k_empty[s], true);
+        }
+        __syncwarp();
       }
       if (i > 0) {
         const int j = i - 1, st = j & 1, s = kVStages == 2 ? st : 0;
@@ -751,16 +780,20 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_mma_kernel(const __grid_co
         if (!wait(&ctl.p_full[st], (j >> 1) & 1, a.fault)) break;
         asm volatile("fence.proxy.async;" ::: "memory");
         tmem_after_sync();
+        if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < kTok / 16; ++k)
-          mma_f16(tmem + kColO + st * kHeadDim, tmem + kColP + st * 32 + 8 * k,
-                  operand(tiles_v + s * kTile + k * 2048, kHalfTile, 1024), kDescO, j >= 2 || k > 0);
-        if (j + kVStages < ntiles) commit<C>(&ctl.v_empty[s], true);
-        commit<C>(&ctl.pv_done[st], false);
+          for (int k = 0; k < kTok / 16; ++k)
+            mma_f16(tmem + kColO + st * kHeadDim, tmem + kColP + st * 32 + 8 * k,
+                    operand(tiles_v + s * kTile + k * 2048, kHalfTile, 1024), kDescO, j >= 2 || k > 0);
+          if (j + kVStages < ntiles) commit<C>(&ctl.v_empty[s], true);
+          commit<C>(&ctl.pv_done[st], false);
+        }
+        __syncwarp();
       }
     }
   }
   __syncwarp();
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   __syncthreads();                                // tiles and codebooks are no longer read
 
   // ---- join the two streams and write this CTA's partial state ----
@@ -785,7 +818,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_mma_kernel(const __grid_co
     const float m1 = second ? ctl.m[r] : -INFINITY, l1 = second ? ctl.l[r] : 0.f;
     const float M = fmaxf(m, m1), ref = M == -INFINITY ? 0.f : M;
     const float f0 = exp2f(m - ref), f1 = exp2f(m1 - ref);
-    const float back = ldexpf(1.f, -ev);
+    const float back = ldexpf(1.f, -book_exponent(1));
 #pragma unroll 1
     for (int c = 0; c < 4; ++c) {
       uint32_t o[32];
@@ -825,25 +858,30 @@ cudaError_t run(const ServeArgs& a, cudaStream_t stream) {
   static PerDeviceFlag flag;
   constexpr int kTiles = (kWide ? 3 : 4) * kTile;
   constexpr size_t kCodes8 = kWide ? 0 : kCodeStages * 2 * C * kTok * R * kGroups;
-  constexpr size_t kMost = kTiles + (kWide ? 2u * R * kWideCodes * 128 : 2u * R * kCodes * (16 / C) * 16) + kCodes8 + sizeof(Control);
+  constexpr size_t kMost = kTiles + 32 * book_items<C, kWide>(R) + kCodes8 + sizeof(Control);
   static_assert(kMost <= 227 * 1024, "fits an SM");
   cudaError_t e = set_smem_limit_once(flag, prefix_mma_kernel<C, kWide, R>, kMost);
   if (e != cudaSuccess) return e;
-  size_t bytes = kTiles + (kWide ? 2u * a.R * kWideCodes * 128 : 2u * R * kCodes * (16 / C) * 16) + kCodes8;
+  prefix_book_kernel<C, kWide><<<dim3(book_items<C, kWide>(a.R) / kBookThreads, 2 * C, a.n_kv_heads), kBookThreads, 0, stream>>>(a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  size_t bytes = kTiles + 32 * static_cast<size_t>(book_items<C, kWide>(a.R)) + kCodes8;
   if (bytes < kOutBytes) bytes = kOutBytes;
   bytes += sizeof(Control);
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = C;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.n_splits * C, a.n_kv_heads, (a.batch * a.group + kRows - 1) / kRows);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = bytes;
   cfg.stream = stream;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, prefix_mma_kernel<C, kWide, R>, a);
 }
 

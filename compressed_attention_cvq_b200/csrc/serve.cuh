@@ -40,6 +40,8 @@ struct ServeArgs {
   const uint8_t* val_codes;
   int R, wide, code_bits;
   PhaseTurns phase;
+  void* book;                     // codebooks in fp16, as the tensor-core kernel holds them
+  uint32_t* book_peak;            // their largest elements
   // paged cache
   const void* k_pages;
   const void* v_pages;

@@ -36,18 +36,22 @@ bool prefix_on_tensor_cores(const cvq_shape* s, int q_dtype) {
   return q_dtype != CVQ_F32 && (!is_wide(s) || s->R <= kWideRoundsPerCta);
 }
 
-// partial states and one arrival counter per (sequence, query head)
-size_t workspace_bytes(int batch, int n_q_heads, int n_parts) {
-  const size_t rows = static_cast<size_t>(batch) * n_q_heads;
-  return round16(rows * n_parts * (kHeadDim + 2) * sizeof(float)) + round16(rows * sizeof(int));
+// partial states of (sequence, query head) rows, 16-byte aligned
+size_t parts_bytes(int batch, int n_q_heads, int n_parts) {
+  return round16(static_cast<size_t>(batch) * n_q_heads * n_parts * (kHeadDim + 2) * sizeof(float));
 }
 
-void place_workspace(ServeArgs& a, void* workspace) {
+// both codebooks of every KV head in fp16
+size_t book_bytes(const cvq_shape* s) {
+  const size_t entries = is_wide(s) ? kWideGroups * kWideCodes * kWideGroupDim : kGroups * kCodes * kCodeword;
+  return 2 * static_cast<size_t>(s->n_kv_heads) * s->R * entries * sizeof(uint16_t);
+}
+
+void place_parts(ServeArgs& a, void* workspace) {
   const size_t rows = static_cast<size_t>(a.batch) * a.n_q_heads * a.n_parts;
   a.part_o = static_cast<float*>(workspace);
   a.part_m = a.part_o + rows * kHeadDim;
   a.part_l = a.part_m + rows;
-  a.counters = reinterpret_cast<int*>(static_cast<char*>(workspace) + round16(rows * (kHeadDim + 2) * sizeof(float)));
 }
 
 cvq_status check_paged(const cvq_paged* p) {
@@ -93,7 +97,8 @@ extern "C" {
 
 size_t cvq_prefix_workspace_bytes(const cvq_shape* s, int n_splits) {
   if (cvq_partials_bytes(s, n_splits) == 0) return 0;
-  return workspace_bytes(s->batch, s->n_q_heads, n_splits * prefix_pair(s));
+  // the book's items of 16 bytes leave one peak per 256
+  return parts_bytes(s->batch, s->n_q_heads, n_splits * prefix_pair(s)) + book_bytes(s) + round16(book_bytes(s) / 1024);
 }
 
 int cvq_prefix_suggest_splits(const cvq_shape* s, int q_dtype, int sm_count) {
@@ -156,7 +161,10 @@ cvq_status cvq_prefix_attend(const cvq_shape* s, const void* q, int q_dtype, con
   a.wide = is_wide(s);
   a.code_bits = s->code_bits == 6 ? 6 : 8;
   phase_turns_host(s->rope_base, &a.phase);
-  place_workspace(a, workspace);
+  place_parts(a, workspace);
+  char* rest = static_cast<char*>(workspace) + parts_bytes(a.batch, a.n_q_heads, a.n_parts);
+  a.book = rest;
+  a.book_peak = reinterpret_cast<uint32_t*>(rest + book_bytes(s));
   if (fault_word_address(&a.fault) != cudaSuccess) return CVQ_ERR_CUDA;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   CVQ_TRY(from_cuda(tensor ? launch_prefix_mma(a, st) : launch_prefix_f32(a, st)));
@@ -165,7 +173,8 @@ cvq_status cvq_prefix_attend(const cvq_shape* s, const void* q, int q_dtype, con
 
 size_t cvq_paged_workspace_bytes(const cvq_paged* p, int n_splits) {
   if (check_paged(p) != CVQ_OK || n_splits < 1 || n_splits > 4096) return 0;
-  return workspace_bytes(p->batch, p->n_q_heads, n_splits);
+  // and one arrival counter per (sequence, KV head)
+  return parts_bytes(p->batch, p->n_q_heads, n_splits) + round16(static_cast<size_t>(p->batch) * p->n_kv_heads * sizeof(int));
 }
 
 int cvq_paged_suggest_splits(const cvq_paged* p, int sm_count) {
@@ -285,7 +294,8 @@ cvq_status cvq_paged_attend(const cvq_paged* p, const void* q, int q_dtype, cons
   a.n_pages = p->n_pages;
   a.max_pages = p->max_pages;
   a.page_stride = stride_of(p);
-  place_workspace(a, workspace);
+  place_parts(a, workspace);
+  a.counters = reinterpret_cast<int*>(static_cast<char*>(workspace) + parts_bytes(a.batch, a.n_q_heads, n_splits));
   if (fault_word_address(&a.fault) != cudaSuccess) return CVQ_ERR_CUDA;
   return from_cuda(launch_paged_attend(a, static_cast<cudaStream_t>(stream)));
 }
