@@ -59,6 +59,7 @@ struct Control {
   uint64_t c_full[kCodeStages], c_empty[kCodeStages];                       // codes
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], pv_done[2];
   uint32_t tmem;
+  int q_exponent[kRows];
   float m[kRows], l[kRows];                       // second stream's state
 };
 
@@ -83,6 +84,10 @@ __device__ __forceinline__ bool wait(uint64_t* bar, unsigned parity, unsigned in
       }
     }
   }
+}
+// by a whole warp, with an answer that the compiler knows to be the same in all lanes
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, unsigned parity, unsigned int* fault) {
+  return __all_sync(0xffffffffu, wait(bar, parity, fault));
 }
 __device__ __forceinline__ void arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
@@ -123,6 +128,14 @@ __device__ __forceinline__ void tmem_load32(uint32_t (&r)[32], uint32_t at) {
 __device__ __forceinline__ void tmem_store32(uint32_t at, const uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::CVQ_V4(r, 0), CVQ_V4(r, 4), CVQ_V4(r, 8), CVQ_V4(r, 12),
+      CVQ_V4(r, 16), CVQ_V4(r, 20), CVQ_V4(r, 24), CVQ_V4(r, 28), "r"(at) : "memory");
+}
+// 16 rows x 64 columns: repetition j holds columns 8 j + 2 (lane % 4), + 1 of rows lane / 4 and
+// lane / 4 + 8
+__device__ __forceinline__ void tmem_store_rows(uint32_t at, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x256b.x8.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
       "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::CVQ_V4(r, 0), CVQ_V4(r, 4), CVQ_V4(r, 8), CVQ_V4(r, 12),
       CVQ_V4(r, 16), CVQ_V4(r, 20), CVQ_V4(r, 24), CVQ_V4(r, 28), "r"(at) : "memory");
 }
@@ -391,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_mma_kernel(const __grid_co
   if (C == 2) cluster_barrier();                  // the other CTA runs, and its barriers are there
   else __syncthreads();
   tmem_after_sync();
-  const uint32_t tmem = ctl.tmem;
+  constexpr uint32_t tmem = 0;                    // all columns: the allocation starts at 0
   // scale exponent of the key (0) or value (1) codebook of this KV head; after the wait for
   // prefix_book_kernel
   auto book_exponent = [&](int values) {
@@ -403,6 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_mma_kernel(const __grid_co
   };
 
   float m = -INFINITY, l = 0.f;                   // softmax: log2 maximum and sum of this thread's row
+  int ev = 0;                                     // exponent of the values' scale
   if (warp < kSoftWarps) {
     // ================= softmax =================
     const int st = warp >> 2, q4 = warp & 3;
@@ -411,39 +425,42 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_mma_kernel(const __grid_co
     // rescaled a few times and not at every tile, and weights stay below 2^(kLift + kSlack)
     constexpr float kLift = 7.f, kSlack = 8.f;
     if (q4 < nact) {
-      // the query row: its scale (both streams), and the operand (first stream)
-      const int r = q4 * 32 + lane;
-      const bool bf16 = a.q_dtype == CVQ_BF16;
-      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + global_row(min(r, nrows - 1)) * kHeadDim);
-      float qmax = 0.f;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const uint4 v = __ldg(src + i);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 f = query_pair(w[j], bf16);
-          qmax = fmaxf(qmax, fmaxf(fabsf(f.x), fabsf(f.y)));
-        }
-      }
-      // largest element to [2^8, 2^9)
-      const int eq = qmax > 0.f && qmax < INFINITY ? 8 - ilogbf(qmax) : 0;
       if (st == 0) {
-        const float up = ldexpf(1.f, min(eq, 127)), rest = ldexpf(1.f, eq - min(eq, 127));
-#pragma unroll
+        // the query operand: 16 rows at a time, 4 lanes a row with 4 elements of every 16 each,
+        // the largest of a row brought to [2^8, 2^9)
+        const bool bf16 = a.q_dtype == CVQ_BF16;
+#pragma unroll 1
         for (int half = 0; half < 2; ++half) {
-          uint32_t out[32];
+          uint32_t x[32];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const uint4 v = __ldg(src + half * 8 + i);
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          for (int k = 0; k < 2; ++k) {
+            const int r = q4 * 32 + 16 * half + 8 * k + (lane >> 2);
+            const uint2* src = reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.q) + global_row(min(r, nrows - 1)) * kHeadDim) + (lane & 3);
+            float mx = 0.f;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float2 f = query_pair(w[j], bf16);
-              out[4 * i + j] = r < nrows ? half_pair(f.x * up * rest, f.y * up * rest) : 0u;
+            for (int j = 0; j < 8; ++j) {
+              const uint2 v = __ldg(src + 4 * j);
+              x[4 * j + 2 * k] = v.x;
+              x[4 * j + 2 * k + 1] = v.y;
+            }
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const float2 f = query_pair(x[4 * (j >> 1) + 2 * k + (j & 1)], bf16);
+              mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
+            }
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            const int eq = mx > 0.f && mx < INFINITY ? 8 - ilogbf(mx) : 0;
+            if ((lane & 3) == 0) ctl.q_exponent[r] = eq;
+            const float up = ldexpf(1.f, min(eq, 127)), rest = ldexpf(1.f, eq - min(eq, 127));
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              uint32_t& w = x[4 * (j >> 1) + 2 * k + (j & 1)];
+              const float2 f = query_pair(w, bf16);
+              w = r < nrows ? half_pair(f.x * up * rest, f.y * up * rest) : 0u;
             }
           }
-          tmem_store32(lanes + kColQ + half * 32, out);
+          tmem_store_rows(lanes + (static_cast<uint32_t>(16 * half) << 16) + kColQ, x);
         }
         tmem_store_wait();
         tmem_before_sync();
@@ -451,7 +468,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_mma_kernel(const __grid_co
         if (lane == 0) arrive(&ctl.q_full);
       }
       asm volatile("griddepcontrol.wait;" ::: "memory");
-      const float factor = ldexpf(0.08838834764831845f * kLog2e, -eq - book_exponent(0));
+      const int ek = book_exponent(0);
+      ev = book_exponent(1);
+      wait(&ctl.q_full, 0, a.fault);
+      const float factor = ldexpf(0.08838834764831845f * kLog2e, -ctl.q_exponent[q4 * 32 + lane] - ek);
       for (int i = st; i < ntiles; i += 2) {
         const unsigned par = (i >> 1) & 1;
         if (!wait(&ctl.s_full[st], par, a.fault)) break;
@@ -550,6 +570,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_mma_kernel(const __grid_co
     Phase ph, step, jump;
     step.set(a.phase, chunk, kWide ? 1 : kSlots);
     if (kWide) jump.set(a.phase, chunk, kGroupTok - 3);
+    auto anchor = [&](int i) {
+      ph.set(a.phase, chunk, static_cast<unsigned long long>(start + static_cast<long long>(i) * kGroupTok + token(0)));
+    };
+    anchor(0);
     const uint32_t my_k = cb_k + cl * 16, my_v = cb_v + cl * 16;
     // 64-scalar groups: a word holds the codes of this slot's 4 tokens for a round; the 8 threads
     // of a slot load two rounds each, a step ahead, and pass them around
@@ -597,8 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_mma_kernel(const __grid_co
       const int s = i & 1;
       if (i >= 2 && !wait(&ctl.k_empty[s], ((i >> 1) - 1) & 1, a.fault)) return false;
       const uint32_t tile = tiles_k + s * kTile;
-      if (i % kReanchor == 0)
-        ph.set(a.phase, chunk, static_cast<unsigned long long>(start + static_cast<long long>(i) * kGroupTok + token(0)));
+      if (i % kReanchor == 0 && i > 0) anchor(i);
       if constexpr (kWide) {
         uint32_t wk[R];
         share_codes(raw_k, wk);
@@ -754,41 +777,45 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_mma_kernel(const __grid_co
     // A tile is two halves of 64 dims, each [64 tokens][128 bytes] with 16-byte chunk c of row t
     // at c ^ (t & 7).  As keys (N = tokens, K = dims, K-major) 8 rows are 1024 bytes apart and 16
     // dims 32 bytes; as values (N = dims, K = tokens, N-major) 64 dims are a half apart and 8
-    // tokens 1024 bytes.
+    // tokens 1024 bytes.  Stages and streams are unrolled so that every operand of the matrix
+    // instructions is in uniform registers (moving them there costs 150 clocks an instruction).
     constexpr uint32_t kDescS = (1u << 4) | ((kTok >> 3) << 17) | ((kRows >> 4) << 24);
     constexpr uint32_t kDescO = (1u << 4) | (1u << 16) | ((kHeadDim >> 3) << 17) | ((kRows >> 4) << 24);
-    bool ok = wait(&ctl.q_full, 0, a.fault);
-    for (int i = 0; ok && i <= ntiles; ++i) {
-      if (i < ntiles) {
-        const int s = i & 1;
-        if (!wait(&ctl.k_full[s], (i >> 1) & 1, a.fault)) break;
-        asm volatile("fence.proxy.async;" ::: "memory");
-        tmem_after_sync();
-        if (elect_one()) {
+    bool ok = warp_wait(&ctl.q_full, 0, a.fault);
+    for (int i0 = 0; ok && i0 <= ntiles; i0 += 2) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            mma_f16(tmem + kColS + s * kTok, tmem + kColQ + 8 * k,
-                    operand(tiles_k + s * kTile + (k >> 2) * kHalfTile + (k & 3) * 32, 16, 1024), kDescS, k > 0);
-          commit<C>(&ctl.s_full[s], false);
-          if (i + 2 < ntiles) commit<C>(&ctl.k_empty[s], true);
-        }
-        __syncwarp();
-      }
-      if (i > 0) {
-        const int j = i - 1, st = j & 1, s = kVStages == 2 ? st : 0;
-        if (!wait(&ctl.v_full[s], (j / kVStages) & 1, a.fault)) break;
-        if (!wait(&ctl.p_full[st], (j >> 1) & 1, a.fault)) break;
-        asm volatile("fence.proxy.async;" ::: "memory");
-        tmem_after_sync();
-        if (elect_one()) {
+      for (int u = 0; u < 2; ++u) {
+        const int i = i0 + u;
+        if (ok && i < ntiles) {
+          ok = warp_wait(&ctl.k_full[u], (i >> 1) & 1, a.fault);
+          if (C == 2) fence_proxy_async_smem();   // the other CTA's stores
+          tmem_after_sync();
+          if (ok && elect_one()) {
 #pragma unroll
-          for (int k = 0; k < kTok / 16; ++k)
-            mma_f16(tmem + kColO + st * kHeadDim, tmem + kColP + st * 32 + 8 * k,
-                    operand(tiles_v + s * kTile + k * 2048, kHalfTile, 1024), kDescO, j >= 2 || k > 0);
-          if (j + kVStages < ntiles) commit<C>(&ctl.v_empty[s], true);
-          commit<C>(&ctl.pv_done[st], false);
+            for (int k = 0; k < 8; ++k)
+              mma_f16(tmem + kColS + u * kTok, tmem + kColQ + 8 * k,
+                      operand(tiles_k + u * kTile + (k >> 2) * kHalfTile + (k & 3) * 32, 16, 1024), kDescS, k > 0);
+            commit<C>(&ctl.s_full[u], false);
+            if (i + 2 < ntiles) commit<C>(&ctl.k_empty[u], true);
+          }
+          __syncwarp();
         }
-        __syncwarp();
+        if (ok && i > 0 && i <= ntiles) {
+          constexpr int kOther[2] = {1, 0};
+          const int j = i - 1, st = kOther[u], s = kVStages == 2 ? kOther[u] : 0;
+          ok = warp_wait(&ctl.v_full[s], (j / kVStages) & 1, a.fault) && warp_wait(&ctl.p_full[st], (j >> 1) & 1, a.fault);
+          if (C == 2) fence_proxy_async_smem();   // the other CTA's stores
+          tmem_after_sync();
+          if (ok && elect_one()) {
+#pragma unroll
+            for (int k = 0; k < kTok / 16; ++k)
+              mma_f16(tmem + kColO + st * kHeadDim, tmem + kColP + st * 32 + 8 * k,
+                      operand(tiles_v + s * kTile + k * 2048, kHalfTile, 1024), kDescO, j >= 2 || k > 0);
+            if (j + kVStages < ntiles) commit<C>(&ctl.v_empty[s], true);
+            commit<C>(&ctl.pv_done[st], false);
+          }
+          __syncwarp();
+        }
       }
     }
   }
@@ -818,7 +845,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_mma_kernel(const __grid_co
     const float m1 = second ? ctl.m[r] : -INFINITY, l1 = second ? ctl.l[r] : 0.f;
     const float M = fmaxf(m, m1), ref = M == -INFINITY ? 0.f : M;
     const float f0 = exp2f(m - ref), f1 = exp2f(m1 - ref);
-    const float back = ldexpf(1.f, -book_exponent(1));
+    const float back = ldexpf(1.f, -ev);
 #pragma unroll 1
     for (int c = 0; c < 4; ++c) {
       uint32_t o[32];
