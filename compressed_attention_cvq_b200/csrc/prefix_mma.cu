@@ -617,104 +617,116 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_mma_kernel(const __grid_co
     // offset of the codeword of word w and token u within a round of a codebook
     const int unit = a.code_bits == 6 ? 6 : 8;
     auto entry = [&](uint32_t w, int u) { return ((w >> (unit * u)) & 63u) * 128u; };
-    auto make_keys = [&](int i) {
-      const int s = i & 1;
-      if (i >= 2 && !wait(&ctl.k_empty[s], ((i >> 1) - 1) & 1, a.fault)) return false;
-      const uint32_t tile = tiles_k + s * kTile;
-      if (i % kReanchor == 0 && i > 0) anchor(i);
-      if constexpr (kWide) {
-        uint32_t wk[R];
-        share_codes(raw_k, wk);
-#pragma unroll
-        for (int u = 0; u < 4; u += 2) {
-          float x[2][8];
-#pragma unroll
-          for (int d = 0; d < 8; ++d) x[0][d] = x[1][d] = 0.f;
-#pragma unroll
-          for (int r = 0; r < R; ++r) {
-            if (r < rounds) {
-              add_chunk(x[0], lds16(my_k + r * (kWideCodes * 128) + entry(wk[r], u)));
-              add_chunk(x[1], lds16(my_k + r * (kWideCodes * 128) + entry(wk[r], u + 1)));
-            }
-          }
-          store(tile, u, ph.rotate(x[0]), &ctl.k_full[s]);
-          ph.turn(step);
-          store(tile, u + 1, ph.rotate(x[1]), &ctl.k_full[s]);
-          if (u == 0) ph.turn(step);
-          else ph.turn(jump);
-        }
-      } else {
-        if (!wait(&ctl.c_full[i % kCodeStages], (i / kCodeStages) & 1, a.fault)) return false;
-        uint32_t w[4 * R];
-#pragma unroll
-        for (int j = 0; j < 4 * R; ++j) w[j] = code(i, 0, j / R, j % R);
-        uint4 v[4 * R];
-#pragma unroll
-        for (int j = 0; j < 4 * R; ++j) v[j] = lds16(my_k + (j % R) * (kCodes * CH * 16) + w[j] * (CH * 16));
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          float x[8];
-          set_chunk(x, v[u * R]);
-#pragma unroll
-          for (int r = 1; r < R; ++r) add_chunk(x, v[u * R + r]);
-          store(tile, u, ph.rotate(x), &ctl.k_full[s]);
-          ph.turn(step);
-        }
-      }
-      publish(&ctl.k_full[s]);
-      if (i + 1 < ntiles) load_codes(a.key_codes, raw_k, i + 1);
-      return true;
-    };
-    auto make_values = [&](int i) {
-      const int s = kVStages == 2 ? i & 1 : 0, lap = i / kVStages;
-      if (lap > 0 && !wait(&ctl.v_empty[s], (lap - 1) & 1, a.fault)) return false;
-      const uint32_t tile = tiles_v + s * kTile;
-      const long long left = end - (start + static_cast<long long>(i) * kGroupTok);
+    // Keys of step i + 1 and values of step i: keys run one step ahead, so that the softmax of a
+    // tile runs under the making of its values; the two are interleaved, so that the gathers of
+    // one run under the arithmetic of the other.
+    auto make = [&](int i) {
+      const bool keys = i + 1 < ntiles, values = i >= 0;
+      const int sk = (i + 1) & 1, sv = kVStages == 2 ? i & 1 : 0, lap = i / kVStages;
+      const uint32_t tile_k = tiles_k + sk * kTile, tile_v = tiles_v + sv * kTile;
+      const long long left = end - (start + static_cast<long long>(i) * kGroupTok);       // of the values' step
       uint4 v[4];
+      if (keys && (i + 1) % kReanchor == 0 && i >= 0) anchor(i + 1);
+      auto keys_free = [&] { return i < 1 || wait(&ctl.k_empty[sk], (((i + 1) >> 1) - 1) & 1, a.fault); };
       if constexpr (kWide) {
-        uint32_t wv[R];
-        share_codes(raw_v, wv);
+        if (keys) {
+          uint32_t wk[R];
+          share_codes(raw_k, wk);
+          if (!keys_free()) return false;
 #pragma unroll
-        for (int u = 0; u < 4; u += 2) {
-          float x[2][8];
+          for (int u = 0; u < 4; u += 2) {
+            float x[2][8];
 #pragma unroll
-          for (int d = 0; d < 8; ++d) x[0][d] = x[1][d] = 0.f;
+            for (int d = 0; d < 8; ++d) x[0][d] = x[1][d] = 0.f;
 #pragma unroll
-          for (int r = 0; r < R; ++r) {
-            if (r < rounds) {
-              add_chunk(x[0], lds16(my_v + r * (kWideCodes * 128) + entry(wv[r], u)));
-              add_chunk(x[1], lds16(my_v + r * (kWideCodes * 128) + entry(wv[r], u + 1)));
+            for (int r = 0; r < R; ++r) {
+              if (r < rounds) {
+                add_chunk(x[0], lds16(my_k + r * (kWideCodes * 128) + entry(wk[r], u)));
+                add_chunk(x[1], lds16(my_k + r * (kWideCodes * 128) + entry(wk[r], u + 1)));
+              }
             }
+            store(tile_k, u, ph.rotate(x[0]), &ctl.k_full[sk]);
+            ph.turn(step);
+            store(tile_k, u + 1, ph.rotate(x[1]), &ctl.k_full[sk]);
+            if (u == 0) ph.turn(step);
+            else ph.turn(jump);
           }
+          publish(&ctl.k_full[sk]);
+          if (i + 2 < ntiles) load_codes(a.key_codes, raw_k, i + 2);
+        }
+        if (values) {
+          uint32_t wv[R];
+          share_codes(raw_v, wv);
 #pragma unroll
-          for (int k = 0; k < 2; ++k)
-            v[u + k] = make_uint4(half_pair(x[k][0], x[k][1]), half_pair(x[k][2], x[k][3]), half_pair(x[k][4], x[k][5]),
-                                  half_pair(x[k][6], x[k][7]));
+          for (int u = 0; u < 4; u += 2) {
+            float x[2][8];
+#pragma unroll
+            for (int d = 0; d < 8; ++d) x[0][d] = x[1][d] = 0.f;
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+              if (r < rounds) {
+                add_chunk(x[0], lds16(my_v + r * (kWideCodes * 128) + entry(wv[r], u)));
+                add_chunk(x[1], lds16(my_v + r * (kWideCodes * 128) + entry(wv[r], u + 1)));
+              }
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+              v[u + k] = make_uint4(half_pair(x[k][0], x[k][1]), half_pair(x[k][2], x[k][3]), half_pair(x[k][4], x[k][5]),
+                                    half_pair(x[k][6], x[k][7]));
+          }
+          if (i + 1 < ntiles) load_codes(a.val_codes, raw_v, i + 1);
         }
       } else {
-        uint32_t w[4 * R];
+        uint32_t wk[4 * R], wv[4 * R];
+        if (values) {
 #pragma unroll
-        for (int j = 0; j < 4 * R; ++j) w[j] = code(i, kCodeBytes, j / R, j % R);
+          for (int j = 0; j < 4 * R; ++j) wv[j] = code(i, kCodeBytes, j / R, j % R);
+        }
+        auto gather_values = [&] {
+          if (!values) return;
 #pragma unroll
-        for (int u = 0; u < 4; ++u) v[u] = lds16(my_v + w[u * R] * (CH * 16));
-        __syncwarp();
-        if (lane == 0) arrive(&ctl.c_empty[i % kCodeStages]);
+          for (int u = 0; u < 4; ++u) {
+            v[u] = lds16(my_v + wv[u * R] * (CH * 16));
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-#pragma unroll
-          for (int r = 1; r < R; ++r) {
-            const uint4 y = lds16(my_v + r * (kCodes * CH * 16) + w[u * R + r] * (CH * 16));
-            v[u] = make_uint4(add_halves(v[u].x, y.x), add_halves(v[u].y, y.y), add_halves(v[u].z, y.z), add_halves(v[u].w, y.w));
+            for (int r = 1; r < R; ++r) {
+              const uint4 y = lds16(my_v + r * (kCodes * CH * 16) + wv[u * R + r] * (CH * 16));
+              v[u] = make_uint4(add_halves(v[u].x, y.x), add_halves(v[u].y, y.y), add_halves(v[u].z, y.z), add_halves(v[u].w, y.w));
+            }
           }
+        };
+        if (keys) {
+          if (!wait(&ctl.c_full[(i + 1) % kCodeStages], ((i + 1) / kCodeStages) & 1, a.fault)) return false;
+#pragma unroll
+          for (int j = 0; j < 4 * R; ++j) wk[j] = code(i + 1, 0, j / R, j % R);
+          uint4 k[4 * R];
+#pragma unroll
+          for (int j = 0; j < 4 * R; ++j) k[j] = lds16(my_k + (j % R) * (kCodes * CH * 16) + wk[j] * (CH * 16));
+          if (R == 1) gather_values();
+          if (!keys_free()) return false;
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            float x[8];
+            set_chunk(x, k[u * R]);
+#pragma unroll
+            for (int r = 1; r < R; ++r) add_chunk(x, k[u * R + r]);
+            store(tile_k, u, ph.rotate(x), &ctl.k_full[sk]);
+            ph.turn(step);
+            if (R > 1 && u == 1) gather_values();
+          }
+          publish(&ctl.k_full[sk]);
+        } else {
+          gather_values();
         }
       }
+      if (!values) return true;
+      if (lap > 0 && !wait(&ctl.v_empty[sv], (lap - 1) & 1, a.fault)) return false;
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         if (token(u) >= left) v[u] = make_uint4(0u, 0u, 0u, 0u);            // weight 0 times this must be 0
-        store(tile, u, v[u], &ctl.v_full[s]);
+        store(tile_v, u, v[u], &ctl.v_full[sv]);
       }
-      publish(&ctl.v_full[s]);
-      if (i + 1 < ntiles) load_codes(a.val_codes, raw_v, i + 1);
+      publish(&ctl.v_full[sv]);
+      if (!kWide && lane == 0) arrive(&ctl.c_empty[i % kCodeStages]);        // publish joined the warp
       return true;
     };
     load_codes(a.key_codes, raw_k, 0);
@@ -734,11 +746,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_mma_kernel(const __grid_co
       }
       asm volatile("bar.sync 1, %0;" ::"n"(kProd) : "memory");
     }
-    bool ok = make_keys(0);                       // keys run one tile ahead of the values
-    for (int i = 0; ok && i < ntiles; ++i) {
-      if (i + 1 < ntiles) ok = make_keys(i + 1);
-      ok = ok && make_values(i);
-    }
+    for (int i = -1; i < ntiles; ++i)
+      if (!make(i)) break;
   } else if (warp == kCopyWarp) {
     // ================= codes =================
     if (lane == 0) {
