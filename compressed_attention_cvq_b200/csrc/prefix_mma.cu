@@ -217,14 +217,8 @@ __device__ __forceinline__ void add_chunk(float (&x)[8], uint4 v) {
     asm("add.f32.f16 %0, %1, %0;" : "+f"(x[2 * i + 1]) : "h"(static_cast<uint16_t>(w[i] >> 16)));
   }
 }
-__device__ __forceinline__ void set_chunk(float (&x)[8], uint4 v) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = floats_of(w[i]);
-    x[2 * i] = f.x;
-    x[2 * i + 1] = f.y;
-  }
+__device__ __forceinline__ uint4 add_chunks(uint4 x, uint4 y) {
+  return make_uint4(add_halves(x.x, y.x), add_halves(x.y, y.y), add_halves(x.z, y.z), add_halves(x.w, y.w));
 }
 
 // e^{i theta_j t} of the 4 pairs of a chunk; packed two pairs at a time
@@ -246,15 +240,30 @@ struct Phase {
       c[p] = nc;
     }
   }
-  // 8 dims (4 interleaved pairs) rotated and rounded
+  // 8 dims of a key, in the order re re im im re re im im, rotated and rounded
   __device__ __forceinline__ uint4 rotate(const float (&x)[8]) const {
     uint32_t w[4];
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
-      const f2 re = pack(x[4 * p], x[4 * p + 2]), im = pack(x[4 * p + 1], x[4 * p + 3]);
+      const f2 re = pack(x[4 * p], x[4 * p + 1]), im = pack(x[4 * p + 2], x[4 * p + 3]);
       const float2 a = unpack(fma2(im, neg2(s[p]), mul2(re, c[p]))), b = unpack(fma2(im, c[p], mul2(re, s[p])));
-      w[2 * p] = half_pair(a.x, b.x);
-      w[2 * p + 1] = half_pair(a.y, b.y);
+      w[2 * p] = half_pair(a.x, a.y);
+      w[2 * p + 1] = half_pair(b.x, b.y);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  // the same in fp16 arithmetic
+  __device__ __forceinline__ uint4 rotate(uint4 k) const {
+    const uint32_t in[4] = {k.x, k.y, k.z, k.w};
+    uint32_t w[4];
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+      const float2 cc = unpack(c[p]), ss = unpack(s[p]);
+      const __half2 co = __floats2half2_rn(cc.x, cc.y), si = __floats2half2_rn(ss.x, ss.y);
+      const __half2 re = *reinterpret_cast<const __half2*>(&in[2 * p]), im = *reinterpret_cast<const __half2*>(&in[2 * p + 1]);
+      const __half2 a = __hfma2(__hneg2(im), si, __hmul2(re, co)), b = __hfma2(im, co, __hmul2(re, si));
+      w[2 * p] = *reinterpret_cast<const uint32_t*>(&a);
+      w[2 * p + 1] = *reinterpret_cast<const uint32_t*>(&b);
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
   }
@@ -274,7 +283,14 @@ template <int C, bool kWide>
 __host__ __device__ constexpr int book_items(int R) {
   return kWide ? R * kWideCodes * 8 : R * kCodes * (16 / C);
 }
-__device__ __forceinline__ uint4 scaled_halves(float4 x, float4 y, float scale) {
+// Keys are held, here and in the operand tiles, with the two real and the two imaginary parts of
+// two pairs side by side, so that a pair of fp16 numbers rotates in one instruction each.
+__device__ __forceinline__ uint4 scaled_halves(float4 x, float4 y, float scale, bool keys) {
+  if (keys) {
+    const float4 a = x, b = y;
+    x = make_float4(a.x, a.z, a.y, a.w);
+    y = make_float4(b.x, b.z, b.y, b.w);
+  }
   return make_uint4(half_pair(x.x * scale, x.y * scale), half_pair(x.z * scale, x.w * scale),
                     half_pair(y.x * scale, y.y * scale), half_pair(y.z * scale, y.w * scale));
 }
@@ -306,7 +322,7 @@ __global__ void __launch_bounds__(kBookThreads) prefix_book_kernel(const __grid_
     if (bits < 0x7f800000u) peak = max(peak, bits);
   }
   reinterpret_cast<uint4*>(a.book)[((static_cast<size_t>(h) * C + rank) * 2 + values) * n + i] =
-      scaled_halves(x, y, static_cast<float>(1 << kUsualScale));
+      scaled_halves(x, y, static_cast<float>(1 << kUsualScale), !values);
   peak = __reduce_max_sync(0xffffffffu, peak);
   if ((threadIdx.x & 31) == 0) warp_peak[threadIdx.x >> 5] = peak;
   __syncthreads();
@@ -454,10 +470,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_mma_kernel(const __grid_co
             if ((lane & 3) == 0) ctl.q_exponent[r] = eq;
             const float up = ldexpf(1.f, min(eq, 127)), rest = ldexpf(1.f, eq - min(eq, 127));
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              uint32_t& w = x[4 * (j >> 1) + 2 * k + (j & 1)];
-              const float2 f = query_pair(w, bf16);
-              w = r < nrows ? half_pair(f.x * up * rest, f.y * up * rest) : 0u;
+            for (int j = 0; j < 8; ++j) {
+              uint32_t &w0 = x[4 * j + 2 * k], &w1 = x[4 * j + 2 * k + 1];
+              const float2 f0 = query_pair(w0, bf16), f1 = query_pair(w1, bf16);
+              w0 = r < nrows ? half_pair(f0.x * up * rest, f1.x * up * rest) : 0u;      // in the keys' order
+              w1 = r < nrows ? half_pair(f0.y * up * rest, f1.y * up * rest) : 0u;
             }
           }
           tmem_store_rows(lanes + (static_cast<uint32_t>(16 * half) << 16) + kColQ, x);
@@ -690,7 +707,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_mma_kernel(const __grid_co
 #pragma unroll
             for (int r = 1; r < R; ++r) {
               const uint4 y = lds16(my_v + r * (kCodes * CH * 16) + wv[u * R + r] * (CH * 16));
-              v[u] = make_uint4(add_halves(v[u].x, y.x), add_halves(v[u].y, y.y), add_halves(v[u].z, y.z), add_halves(v[u].w, y.w));
+              v[u] = add_chunks(v[u], y);
             }
           }
         };
@@ -705,11 +722,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_mma_kernel(const __grid_co
           if (!keys_free()) return false;
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
-            float x[8];
-            set_chunk(x, k[u * R]);
 #pragma unroll
-            for (int r = 1; r < R; ++r) add_chunk(x, k[u * R + r]);
-            store(tile_k, u, ph.rotate(x), &ctl.k_full[sk]);
+            for (int r = 1; r < R; ++r) k[u * R] = add_chunks(k[u * R], k[u * R + r]);
+            store(tile_k, u, ph.rotate(k[u * R]), &ctl.k_full[sk]);
             ph.turn(step);
             if (R > 1 && u == 1) gather_values();
           }
@@ -741,8 +756,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_mma_kernel(const __grid_co
       for (int i = tid; i < book_items<C, kWide>(rounds); i += kProd) {
         const float4* k = reinterpret_cast<const float4*>(book_item<C, kWide>(kcb, rounds, rank, i));
         const float4* v = reinterpret_cast<const float4*>(book_item<C, kWide>(vcb, rounds, rank, i));
-        sts16(cb_k + i * 16, scaled_halves(__ldg(k), __ldg(k + 1), ldexpf(1.f, ek)));
-        sts16(cb_v + i * 16, scaled_halves(__ldg(v), __ldg(v + 1), ldexpf(1.f, ev)));
+        sts16(cb_k + i * 16, scaled_halves(__ldg(k), __ldg(k + 1), ldexpf(1.f, ek), true));
+        sts16(cb_v + i * 16, scaled_halves(__ldg(v), __ldg(v + 1), ldexpf(1.f, ev), false));
       }
       asm volatile("bar.sync 1, %0;" ::"n"(kProd) : "memory");
     }
