@@ -6,8 +6,8 @@
 // tokens, in tiles of 64:
 //   producers (8 warps)  gather codewords from fp16 codebooks in shared memory, sum the
 //                        rounds, rotate the keys and store key and value tiles
-//   one thread           copies the codes of four steps ahead into shared memory (8-scalar groups)
-//   one thread           S = Q K^T (M = 128 rows, N = 64 tokens; Q from TMEM), O += P V
+//   one thread           copies codes, steps ahead, into shared memory (8-scalar groups)
+//   two threads          S = Q K^T (M = 128 rows, N = 64 tokens; Q from TMEM), O += P V
 //                        (N = 128 dims; P from TMEM), both tcgen05.mma kind::f16
 //   softmax (2 x 4 warps)  a thread owns a row: even tiles go to the first four warps, odd
 //                        ones to the others, each with its own O, maximum and sum (joined at
@@ -40,13 +40,13 @@ namespace {
 constexpr int kSoftWarps = 8;
 constexpr int kProdWarps = 8;
 constexpr int kProd = 32 * kProdWarps;
-constexpr int kMmaWarp = kSoftWarps + kProdWarps, kCopyWarp = kMmaWarp + 1;
+constexpr int kScoreWarp = kSoftWarps + kProdWarps, kOutWarp = kScoreWarp + 1, kCopyWarp = kOutWarp + 1;
 constexpr int kThreads = 32 * (kCopyWarp + 1);
 constexpr int kRows = 128;
 constexpr int kTok = 64;                          // tokens of a tile
 constexpr int kHalfTile = kTok * 128;             // 64 dims of its keys or values, bytes
 constexpr int kTile = 2 * kHalfTile;
-constexpr int kCodeStages = 4;
+constexpr int kMostCodeStages = 8;                // what a CTA alone has room for; a pair has for 4
 constexpr int kReanchor = 64;                     // tiles between exact phases
 constexpr int kOutPitch = kHeadDim + 4;           // floats; 16-byte chunks of 8 rows in 8 bank groups
 constexpr int kOutBytes = kRows * kOutPitch * 4;
@@ -56,8 +56,8 @@ constexpr uint32_t kColS = 0, kColP = 128, kColQ = 192, kColO = 256, kTmemCols =
 struct Control {
   uint64_t book;                                  // codebooks
   uint64_t q_full;
-  uint64_t c_full[kCodeStages], c_empty[kCodeStages];                       // codes
-  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], pv_done[2];
+  uint64_t c_full[2][kMostCodeStages], c_empty[2][kMostCodeStages];         // codes of keys, values
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], s_empty[2], p_full[2], pv_done[2];
   uint32_t tmem;
   int q_exponent[kRows];
   float m[kRows], l[kRows];                       // second stream's state
@@ -70,7 +70,7 @@ __device__ __forceinline__ bool wait(uint64_t* bar, unsigned parity, unsigned in
   for (unsigned i = 1;; ++i) {
     uint32_t done;
     asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
         " selp.u32 %0, 1, 0, p;\n}"
         : "=r"(done) : "r"(addr), "r"(parity) : "memory");
     if (done) return true;
@@ -84,10 +84,6 @@ __device__ __forceinline__ bool wait(uint64_t* bar, unsigned parity, unsigned in
       }
     }
   }
-}
-// by a whole warp, with an answer that the compiler knows to be the same in all lanes
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, unsigned parity, unsigned int* fault) {
-  return __all_sync(0xffffffffu, wait(bar, parity, fault));
 }
 __device__ __forceinline__ void arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
@@ -350,6 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_mma_kernel(const __grid_co
   constexpr int CH = 16 / C;
   constexpr int kSlots = kProd / CH;              // tokens that the producers take at once; 4 in turn
   constexpr int kVStages = kWide ? 1 : 2;
+  constexpr int kCodeStages = kMostCodeStages / C;
   static_assert(kSlots * 4 == kGroupTok, "a producer thread takes 4 tokens a step");
   static_assert(!kWide || C == 2, "a CTA holds one 64-scalar group");
   extern __shared__ __align__(1024) unsigned char smem[];
@@ -393,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_mma_kernel(const __grid_co
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");          // the merge
 
   // ---- set-up ----
-  if (warp == kMmaWarp) {
+  if (warp == kScoreWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&ctl.tmem)), "r"(kTmemCols) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   } else if (warp == kCopyWarp && lane == 0) {
@@ -406,13 +403,17 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_mma_kernel(const __grid_co
       mbar_init(&ctl.k_empty[s], C);
       mbar_init(&ctl.v_empty[s], C);
       mbar_init(&ctl.s_full[s], 1);
+      mbar_init(&ctl.s_empty[s], nact);
       mbar_init(&ctl.p_full[s], nact);
       mbar_init(&ctl.pv_done[s], 1);
     }
 #pragma unroll
     for (int s = 0; s < kCodeStages; ++s) {
-      mbar_init(&ctl.c_full[s], 1);
-      mbar_init(&ctl.c_empty[s], kProdWarps);
+#pragma unroll
+      for (int v = 0; v < 2; ++v) {
+        mbar_init(&ctl.c_full[v][s], 1);
+        mbar_init(&ctl.c_empty[v][s], kProdWarps);
+      }
     }
   }
   __syncwarp();
@@ -497,6 +498,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_mma_kernel(const __grid_co
         tmem_load32(s0, lanes + kColS + st * kTok);
         tmem_load32(s1, lanes + kColS + st * kTok + 32);
         tmem_load_wait();
+        tmem_before_sync();
+        __syncwarp();
+        if (lane == 0) arrive(&ctl.s_empty[st]);  // the next scores of this stream may come
         const long long left = end - (start + static_cast<long long>(i) * kGroupTok + rank * kTok);
         if (left < kTok) {
 #pragma unroll
@@ -505,9 +509,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_mma_kernel(const __grid_co
             if (j + 32 >= left) s1[j] = 0xff800000u;
           }
         }
-        float mx = -INFINITY;
+        float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int j = 0; j < 32; ++j) mx = fmaxf(mx, fmaxf(__uint_as_float(s0[j]), __uint_as_float(s1[j])));
+        for (int j = 0; j < 32; ++j) mx4[j & 3] = fmaxf(mx4[j & 3], fmaxf(__uint_as_float(s0[j]), __uint_as_float(s1[j])));
+        float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
         mx *= factor;
         const bool grow = mx > m + kSlack || (m == -INFINITY && mx > m);
         const float alpha = grow ? exp2f(m - mx) : 1.f;
@@ -634,17 +639,18 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_mma_kernel(const __grid_co
     // offset of the codeword of word w and token u within a round of a codebook
     const int unit = a.code_bits == 6 ? 6 : 8;
     auto entry = [&](uint32_t w, int u) { return ((w >> (unit * u)) & 63u) * 128u; };
-    // Keys of step i + 1 and values of step i: keys run one step ahead, so that the softmax of a
+    // Keys of step i + 2 and values of step i: keys run two steps ahead, so that the softmax of a
     // tile runs under the making of its values; the two are interleaved, so that the gathers of
     // one run under the arithmetic of the other.
     auto make = [&](int i) {
-      const bool keys = i + 1 < ntiles, values = i >= 0;
-      const int sk = (i + 1) & 1, sv = kVStages == 2 ? i & 1 : 0, lap = i / kVStages;
+      const int ik = i + 2;
+      const bool keys = ik < ntiles, values = i >= 0;
+      const int sk = ik & 1, sv = kVStages == 2 ? i & 1 : 0, lap = i / kVStages;
       const uint32_t tile_k = tiles_k + sk * kTile, tile_v = tiles_v + sv * kTile;
       const long long left = end - (start + static_cast<long long>(i) * kGroupTok);       // of the values' step
       uint4 v[4];
-      if (keys && (i + 1) % kReanchor == 0 && i >= 0) anchor(i + 1);
-      auto keys_free = [&] { return i < 1 || wait(&ctl.k_empty[sk], (((i + 1) >> 1) - 1) & 1, a.fault); };
+      if (keys && ik % kReanchor == 0 && ik > 0) anchor(ik);
+      auto keys_free = [&] { return ik < 2 || wait(&ctl.k_empty[sk], ((ik >> 1) - 1) & 1, a.fault); };
       if constexpr (kWide) {
         if (keys) {
           uint32_t wk[R];
@@ -669,7 +675,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_mma_kernel(const __grid_co
             else ph.turn(jump);
           }
           publish(&ctl.k_full[sk]);
-          if (i + 2 < ntiles) load_codes(a.key_codes, raw_k, i + 2);
+          if (ik + 1 < ntiles) load_codes(a.key_codes, raw_k, ik + 1);
         }
         if (values) {
           uint32_t wv[R];
@@ -696,6 +702,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_mma_kernel(const __grid_co
       } else {
         uint32_t wk[4 * R], wv[4 * R];
         if (values) {
+          if (!wait(&ctl.c_full[1][i % kCodeStages], (i / kCodeStages) & 1, a.fault)) return false;
 #pragma unroll
           for (int j = 0; j < 4 * R; ++j) wv[j] = code(i, kCodeBytes, j / R, j % R);
         }
@@ -712,9 +719,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_mma_kernel(const __grid_co
           }
         };
         if (keys) {
-          if (!wait(&ctl.c_full[(i + 1) % kCodeStages], ((i + 1) / kCodeStages) & 1, a.fault)) return false;
+          if (!wait(&ctl.c_full[0][ik % kCodeStages], (ik / kCodeStages) & 1, a.fault)) return false;
 #pragma unroll
-          for (int j = 0; j < 4 * R; ++j) wk[j] = code(i + 1, 0, j / R, j % R);
+          for (int j = 0; j < 4 * R; ++j) wk[j] = code(ik, 0, j / R, j % R);
           uint4 k[4 * R];
 #pragma unroll
           for (int j = 0; j < 4 * R; ++j) k[j] = lds16(my_k + (j % R) * (kCodes * CH * 16) + wk[j] * (CH * 16));
@@ -729,6 +736,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_mma_kernel(const __grid_co
             if (R > 1 && u == 1) gather_values();
           }
           publish(&ctl.k_full[sk]);
+          if (lane == 0) arrive(&ctl.c_empty[0][ik % kCodeStages]);          // publish joined the warp
         } else {
           gather_values();
         }
@@ -741,7 +749,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_mma_kernel(const __grid_co
         store(tile_v, u, v[u], &ctl.v_full[sv]);
       }
       publish(&ctl.v_full[sv]);
-      if (!kWide && lane == 0) arrive(&ctl.c_empty[i % kCodeStages]);        // publish joined the warp
+      if (!kWide && lane == 0) arrive(&ctl.c_empty[1][i % kCodeStages]);
       return true;
     };
     load_codes(a.key_codes, raw_k, 0);
@@ -761,26 +769,28 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_mma_kernel(const __grid_co
       }
       asm volatile("bar.sync 1, %0;" ::"n"(kProd) : "memory");
     }
-    for (int i = -1; i < ntiles; ++i)
+    for (int i = -2; i < ntiles; ++i)
       if (!make(i)) break;
   } else if (warp == kCopyWarp) {
     // ================= codes =================
     if (lane == 0) {
       const size_t row = static_cast<size_t>(R) * kGroups;
-      auto copy_codes = [&](int i) {
+      auto copy_codes = [&](int i, int values) {
         const int s = i % kCodeStages;
-        if (i >= kCodeStages && !wait(&ctl.c_empty[s], (i / kCodeStages - 1) & 1, a.fault)) return false;
+        uint64_t* full = &ctl.c_full[values][s];
+        if (i >= kCodeStages && !wait(&ctl.c_empty[values][s], (i / kCodeStages - 1) & 1, a.fault)) return false;
         const long long t = start + static_cast<long long>(i) * kGroupTok;
         const uint32_t bytes = static_cast<uint32_t>(min(end - t, static_cast<long long>(kGroupTok))) * static_cast<uint32_t>(row);
-        const size_t at = (static_cast<size_t>(h) * a.t_cap + t) * row;
-        unsigned char* dst = smem + (ring - tiles_k) + s * (2 * kCodeBytes);
-        mbar_expect_tx(&ctl.c_full[s], 2 * bytes);
-        bulk_load(dst, a.key_codes + at, bytes, &ctl.c_full[s]);
-        bulk_load(dst + kCodeBytes, a.val_codes + at, bytes, &ctl.c_full[s]);
+        mbar_expect_tx(full, bytes);
+        bulk_load(smem + (ring - tiles_k) + s * (2 * kCodeBytes) + values * kCodeBytes,
+                  (values ? a.val_codes : a.key_codes) + (static_cast<size_t>(h) * a.t_cap + t) * row, bytes, full);
         return true;
       };
       const int first = kWide ? 0 : min(ntiles, kCodeStages);
-      for (int i = 0; i < first; ++i) copy_codes(i);
+      for (int i = 0; i < first; ++i) {
+        copy_codes(i, 0);
+        copy_codes(i, 1);
+      }
       asm volatile("griddepcontrol.wait;" ::: "memory");
       constexpr uint32_t kPiece = 16384;
       mbar_expect_tx(&ctl.book, 2 * cb_bytes);
@@ -789,57 +799,53 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_mma_kernel(const __grid_co
         bulk_load(smem + (cb_k - tiles_k) + at, book + at, min(kPiece, 2 * cb_bytes - at), &ctl.book);
       if (!kWide) {
         bool ok = true;
-        for (int i = first; ok && i < ntiles; ++i) ok = copy_codes(i);
+        for (int i = first; ok && i < ntiles + 2; ++i) {                   // values are two steps behind
+          if (i < ntiles) ok = copy_codes(i, 0);
+          if (ok && i - 2 >= first) ok = copy_codes(i - 2, 1);
+        }
         // no copy is left in flight, whatever ended the others' loops
         for (int i = max(0, ntiles - kCodeStages); ok && i < ntiles; ++i)
-          ok = wait(&ctl.c_full[i % kCodeStages], (i / kCodeStages) & 1, a.fault);
+          ok = wait(&ctl.c_full[0][i % kCodeStages], (i / kCodeStages) & 1, a.fault) &&
+               wait(&ctl.c_full[1][i % kCodeStages], (i / kCodeStages) & 1, a.fault);
       }
       wait(&ctl.book, 0, a.fault);
     }
-  } else {
+  } else if (elect_one()) {
     // ================= matrix products =================
     // A tile is two halves of 64 dims, each [64 tokens][128 bytes] with 16-byte chunk c of row t
     // at c ^ (t & 7).  As keys (N = tokens, K = dims, K-major) 8 rows are 1024 bytes apart and 16
     // dims 32 bytes; as values (N = dims, K = tokens, N-major) 64 dims are a half apart and 8
-    // tokens 1024 bytes.  Stages and streams are unrolled so that every operand of the matrix
-    // instructions is in uniform registers (moving them there costs 150 clocks an instruction).
+    // tokens 1024 bytes.  Scores and outputs are issued by a warp each: the waits and issue of
+    // both in one took longer than the products.
     constexpr uint32_t kDescS = (1u << 4) | ((kTok >> 3) << 17) | ((kRows >> 4) << 24);
     constexpr uint32_t kDescO = (1u << 4) | (1u << 16) | ((kHeadDim >> 3) << 17) | ((kRows >> 4) << 24);
-    bool ok = warp_wait(&ctl.q_full, 0, a.fault);
-    for (int i0 = 0; ok && i0 <= ntiles; i0 += 2) {
+    if (warp == kScoreWarp) {
+      bool ok = wait(&ctl.q_full, 0, a.fault);
+      for (int i = 0; ok && i < ntiles; ++i) {
+        const int u = i & 1;
+        ok = wait(&ctl.k_full[u], (i >> 1) & 1, a.fault) && (i < 2 || wait(&ctl.s_empty[u], ((i >> 1) - 1) & 1, a.fault));
+        if (!ok) break;
+        if (C == 2) fence_proxy_async_smem();     // the other CTA's stores
+        tmem_after_sync();
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int i = i0 + u;
-        if (ok && i < ntiles) {
-          ok = warp_wait(&ctl.k_full[u], (i >> 1) & 1, a.fault);
-          if (C == 2) fence_proxy_async_smem();   // the other CTA's stores
-          tmem_after_sync();
-          if (ok && elect_one()) {
+        for (int k = 0; k < 8; ++k)
+          mma_f16(tmem + kColS + u * kTok, tmem + kColQ + 8 * k,
+                  operand(tiles_k + u * kTile + (k >> 2) * kHalfTile + (k & 3) * 32, 16, 1024), kDescS, k > 0);
+        commit<C>(&ctl.s_full[u], false);
+        if (i + 2 < ntiles) commit<C>(&ctl.k_empty[u], true);
+      }
+    } else {
+      for (int i = 0; i < ntiles; ++i) {
+        const int u = i & 1, s = kVStages == 2 ? u : 0;
+        if (!wait(&ctl.v_full[s], (i / kVStages) & 1, a.fault) || !wait(&ctl.p_full[u], (i >> 1) & 1, a.fault)) break;
+        if (C == 2) fence_proxy_async_smem();
+        tmem_after_sync();
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              mma_f16(tmem + kColS + u * kTok, tmem + kColQ + 8 * k,
-                      operand(tiles_k + u * kTile + (k >> 2) * kHalfTile + (k & 3) * 32, 16, 1024), kDescS, k > 0);
-            commit<C>(&ctl.s_full[u], false);
-            if (i + 2 < ntiles) commit<C>(&ctl.k_empty[u], true);
-          }
-          __syncwarp();
-        }
-        if (ok && i > 0 && i <= ntiles) {
-          constexpr int kOther[2] = {1, 0};
-          const int j = i - 1, st = kOther[u], s = kVStages == 2 ? kOther[u] : 0;
-          ok = warp_wait(&ctl.v_full[s], (j / kVStages) & 1, a.fault) && warp_wait(&ctl.p_full[st], (j >> 1) & 1, a.fault);
-          if (C == 2) fence_proxy_async_smem();   // the other CTA's stores
-          tmem_after_sync();
-          if (ok && elect_one()) {
-#pragma unroll
-            for (int k = 0; k < kTok / 16; ++k)
-              mma_f16(tmem + kColO + st * kHeadDim, tmem + kColP + st * 32 + 8 * k,
-                      operand(tiles_v + s * kTile + k * 2048, kHalfTile, 1024), kDescO, j >= 2 || k > 0);
-            if (j + kVStages < ntiles) commit<C>(&ctl.v_empty[s], true);
-            commit<C>(&ctl.pv_done[st], false);
-          }
-          __syncwarp();
-        }
+        for (int k = 0; k < kTok / 16; ++k)
+          mma_f16(tmem + kColO + u * kHeadDim, tmem + kColP + u * 32 + 8 * k,
+                  operand(tiles_v + s * kTile + k * 2048, kHalfTile, 1024), kDescO, i >= 2 || k > 0);
+        if (i + kVStages < ntiles) commit<C>(&ctl.v_empty[s], true);
+        commit<C>(&ctl.pv_done[u], false);
       }
     }
   }
@@ -899,7 +905,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_mma_kernel(const __grid_co
     *reinterpret_cast<float4*>(a.part_o + (global_row(rr) * n_parts + blockIdx.x) * kHeadDim + c) =
         *reinterpret_cast<const float4*>(rows_out + rr * kOutPitch + c);
   }
-  if (warp == kMmaWarp)
+  if (warp == kScoreWarp)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
   if (C == 2) cluster_barrier();                  // the other CTA may still store here until now
 }
@@ -908,7 +914,7 @@ template <int C, bool kWide, int R>
 cudaError_t run(const ServeArgs& a, cudaStream_t stream) {
   static PerDeviceFlag flag;
   constexpr int kTiles = (kWide ? 3 : 4) * kTile;
-  constexpr size_t kCodes8 = kWide ? 0 : kCodeStages * 2 * C * kTok * R * kGroups;
+  constexpr size_t kCodes8 = kWide ? 0 : kMostCodeStages / C * 2 * C * kTok * R * kGroups;
   constexpr size_t kMost = kTiles + 32 * book_items<C, kWide>(R) + kCodes8 + sizeof(Control);
   static_assert(kMost <= 227 * 1024, "fits an SM");
   cudaError_t e = set_smem_limit_once(flag, prefix_mma_kernel<C, kWide, R>, kMost);
