@@ -10,6 +10,9 @@ compressed_attention_cvq_b200/libcvq.so.  The debug build compiles the same sour
 -DCVQ_DEBUG_BOUNDS (device-side range checks that set CVQ_FAULT_BOUNDS in the fault word
 and skip the access) into _build_debug/ and compressed_attention_cvq_b200/libcvq_debug.so,
 which the binding loads when CVQ_LIBRARY=debug.
+
+csrc/serving_module.cpp becomes the Python module compressed_attention_cvq_b200/_serving.so
+(g++, against torch's headers): the argument checks of the serving calls.
 """
 from __future__ import annotations
 
@@ -27,6 +30,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libcvq.so")
+MODULE_SRC = os.path.join(CSRC, "serving_module.cpp")
+MODULE = os.path.join(PKG, "_serving.so")
 BUILD_DEBUG = os.path.join(ROOT, "_build_debug")
 LIB_DEBUG = os.path.join(PKG, "libcvq_debug.so")
 
@@ -84,7 +89,30 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    _build_module(force, verbose)
     return lib_path
+
+
+def _build_module(force: bool, verbose: bool) -> None:
+    if not force and not _stale(MODULE, MODULE_SRC):
+        return
+    import sysconfig
+
+    import torch
+    from torch.utils.cpp_extension import include_paths
+
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    inc = [INCLUDE, *include_paths(), sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *(x for d in inc for x in ("-I", d)), MODULE_SRC, "-o", MODULE,
+           "-L", os.path.join(os.path.dirname(torch.__file__), "lib"), "-lc10", "-lc10_cuda",
+           "-ltorch_cpu", "-ltorch", "-ltorch_python"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {MODULE_SRC}:\n{r.stdout}\n{r.stderr}")
 
 
 def main(argv=None):

@@ -743,11 +743,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_mma_kernel(const __grid_co
       }
       if (!values) return true;
       if (lap > 0 && !wait(&ctl.v_empty[sv], (lap - 1) & 1, a.fault)) return false;
+      if (left < kGroupTok) {
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        if (token(u) >= left) v[u] = make_uint4(0u, 0u, 0u, 0u);            // weight 0 times this must be 0
-        store(tile_v, u, v[u], &ctl.v_full[sv]);
+        for (int u = 0; u < 4; ++u)
+          if (token(u) >= left) v[u] = make_uint4(0u, 0u, 0u, 0u);          // weight 0 times this must be 0
       }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) store(tile_v, u, v[u], &ctl.v_full[sv]);
       publish(&ctl.v_full[sv]);
       if (!kWide && lane == 0) arrive(&ctl.c_empty[1][i % kCodeStages]);
       return true;
