@@ -4,7 +4,7 @@
 //
 // A CTA takes 128 query rows ((sequence, head of the group) pairs) of a KV head and a run of
 // tokens, in tiles of 64:
-//   producers (8 warps)  gather codewords from fp16 codebooks in shared memory, sum the
+//   producers            gather codewords from fp16 codebooks in shared memory, sum the
 //                        rounds, rotate the keys and store key and value tiles
 //   one thread           copies codes, steps ahead, into shared memory (8-scalar groups)
 //   two threads          S = Q K^T (M = 128 rows, N = 64 tokens; Q from TMEM), O += P V
@@ -38,10 +38,15 @@ namespace cvq {
 namespace {
 
 constexpr int kSoftWarps = 8;
-constexpr int kProdWarps = 8;
-constexpr int kProd = 32 * kProdWarps;
-constexpr int kScoreWarp = kSoftWarps + kProdWarps, kOutWarp = kScoreWarp + 1, kCopyWarp = kOutWarp + 1;
-constexpr int kThreads = 32 * (kCopyWarp + 1);
+// The warps by their roles.  Eight producer warps for 8-scalar groups; the many gathers of a
+// 64-scalar group want sixteen, in fewer registers each.
+template <bool kWide>
+struct Roles {
+  static constexpr int kProdWarps = kWide ? 16 : 8;
+  static constexpr int kProd = 32 * kProdWarps;
+  static constexpr int kScoreWarp = kSoftWarps + kProdWarps, kOutWarp = kScoreWarp + 1, kCopyWarp = kOutWarp + 1;
+  static constexpr int kThreads = 32 * (kCopyWarp + 1);
+};
 constexpr int kRows = 128;
 constexpr int kTok = 64;                          // tokens of a tile
 constexpr int kHalfTile = kTok * 128;             // 64 dims of its keys or values, bytes
@@ -341,13 +346,17 @@ __device__ __forceinline__ float2 query_pair(uint32_t w, bool bf16) {
 
 // kWide: R is the most rounds; the call's own number is a.R
 template <int C, bool kWide, int R>
-__global__ void __launch_bounds__(kThreads, 1) prefix_mma_kernel(const __grid_constant__ ServeArgs a) {
+__global__ void __launch_bounds__(Roles<kWide>::kThreads, 1) prefix_mma_kernel(const __grid_constant__ ServeArgs a) {
+  using W = Roles<kWide>;
+  constexpr int kProdWarps = W::kProdWarps, kProd = W::kProd, kThreads = W::kThreads;
+  constexpr int kScoreWarp = W::kScoreWarp, kCopyWarp = W::kCopyWarp;
   constexpr int kGroupTok = C * kTok;             // tokens of a step of the CTA or pair
   constexpr int CH = 16 / C;
-  constexpr int kSlots = kProd / CH;              // tokens that the producers take at once; 4 in turn
+  constexpr int kSlots = kProd / CH;              // tokens that the producers take at once
+  constexpr int kPer = kGroupTok / kSlots;        // tokens of a producer thread in a step
   constexpr int kVStages = kWide ? 1 : 2;
   constexpr int kCodeStages = kMostCodeStages / C;
-  static_assert(kSlots * 4 == kGroupTok, "a producer thread takes 4 tokens a step");
+  static_assert(kPer * kSlots == kGroupTok && kPer == (kWide ? 2 : 4), "the code below");
   static_assert(!kWide || C == 2, "a CTA holds one 64-scalar group");
   extern __shared__ __align__(1024) unsigned char smem[];
   const uint32_t tiles_k = smem_u32(smem), tiles_v = tiles_k + 2 * kTile;
@@ -494,24 +503,33 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_mma_kernel(const __grid_co
         const unsigned par = (i >> 1) & 1;
         if (!wait(&ctl.s_full[st], par, a.fault)) break;
         tmem_after_sync();
-        uint32_t s0[32], s1[32];
-        tmem_load32(s0, lanes + kColS + st * kTok);
-        tmem_load32(s1, lanes + kColS + st * kTok + 32);
-        tmem_load_wait();
-        tmem_before_sync();
-        __syncwarp();
-        if (lane == 0) arrive(&ctl.s_empty[st]);  // the next scores of this stream may come
+        // 64 scores, held at once where the registers allow it and else read twice
+        constexpr int kHeld = kWide ? 1 : 2;
         const long long left = end - (start + static_cast<long long>(i) * kGroupTok + rank * kTok);
-        if (left < kTok) {
+        uint32_t s[kHeld][32];
+        auto load_scores = [&](int c, uint32_t (&x)[32]) {
+          tmem_load32(x, lanes + kColS + st * kTok + 32 * c);
+          tmem_load_wait();
+          if (left < kTok) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            if (j >= left) s0[j] = 0xff800000u;
-            if (j + 32 >= left) s1[j] = 0xff800000u;
+            for (int j = 0; j < 32; ++j)
+              if (32 * c + j >= left) x[j] = 0xff800000u;
           }
-        }
+        };
+        auto scores_read = [&] {                  // the next scores of this stream may come
+          tmem_before_sync();
+          __syncwarp();
+          if (lane == 0) arrive(&ctl.s_empty[st]);
+        };
         float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int j = 0; j < 32; ++j) mx4[j & 3] = fmaxf(mx4[j & 3], fmaxf(__uint_as_float(s0[j]), __uint_as_float(s1[j])));
+        for (int c = 1; c >= 0; --c) {
+          load_scores(c, s[c % kHeld]);
+#pragma unroll
+          for (int j = 0; j < 32; j += 2)
+            mx4[j / 2 & 3] = fmaxf(mx4[j / 2 & 3], fmaxf(__uint_as_float(s[c % kHeld][j]), __uint_as_float(s[c % kHeld][j + 1])));
+        }
+        if (kHeld == 2) scores_read();
         float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
         mx *= factor;
         const bool grow = mx > m + kSlack || (m == -INFINITY && mx > m);
@@ -522,13 +540,19 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_mma_kernel(const __grid_co
         f2 sum = 0;
         uint32_t p[32];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const float2 x = unpack(fma2(pack(__uint_as_float(s0[2 * j]), __uint_as_float(s0[2 * j + 1])), ff, rr));
-          const float2 y = unpack(fma2(pack(__uint_as_float(s1[2 * j]), __uint_as_float(s1[2 * j + 1])), ff, rr));
-          const float e0 = exp2_fast(x.x), e1 = exp2_fast(x.y), e2 = exp2_fast(y.x), e3 = exp2_fast(y.y);
-          sum = add2(sum, add2(pack(e0, e1), pack(e2, e3)));
-          p[j] = half_pair(e0, e1);
-          p[16 + j] = half_pair(e2, e3);
+        for (int c = 0; c < 2; ++c) {
+          if (kHeld == 1 && c == 1) {
+            load_scores(1, s[0]);
+            scores_read();
+          }
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const uint32_t(&x)[32] = s[c % kHeld];
+            const float2 y = unpack(fma2(pack(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])), ff, rr));
+            const float e0 = exp2_fast(y.x), e1 = exp2_fast(y.y);
+            sum = add2(sum, pack(e0, e1));
+            p[16 * c + j] = half_pair(e0, e1);
+          }
         }
         const float2 sums = unpack(sum);
         l = fmaf(l, alpha, sums.x + sums.y);
@@ -565,11 +589,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_mma_kernel(const __grid_co
     const int cl = tid % CH, slot = tid / CH;
     const int chunk = C == 2 ? 8 * rank + cl : cl;
     // token u of this thread within a step, the CTA it belongs to and its row of the tile there
-    auto token = [&](int u) { return kWide ? 4 * slot + u : slot + u * kSlots; };
-    uint32_t at[4];                               // of its 16 bytes, from the start of a tile
-    bool mine[4];
+    auto token = [&](int u) { return kWide ? kPer * slot + u : slot + u * kSlots; };
+    uint32_t at[kPer];                            // of its 16 bytes, from the start of a tile
+    bool mine[kPer];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
+    for (int u = 0; u < kPer; ++u) {
       const int row = token(u) % kTok, to = C == 2 ? token(u) / kTok : 0;
       mine[u] = to == rank;
       at[u] = (chunk >> 3) * kHalfTile + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);
@@ -591,13 +615,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_mma_kernel(const __grid_co
     };
     Phase ph, step, jump;
     step.set(a.phase, chunk, kWide ? 1 : kSlots);
-    if (kWide) jump.set(a.phase, chunk, kGroupTok - 3);
+    if (kWide) jump.set(a.phase, chunk, kGroupTok - (kPer - 1));
     auto anchor = [&](int i) {
       ph.set(a.phase, chunk, static_cast<unsigned long long>(start + static_cast<long long>(i) * kGroupTok + token(0)));
     };
     anchor(0);
     const uint32_t my_k = cb_k + cl * 16, my_v = cb_v + cl * 16;
-    // 64-scalar groups: a word holds the codes of this slot's 4 tokens for a round; the 8 threads
+    // 64-scalar groups: a word holds the codes of 4 tokens, two slots', for a round; the 8 threads
     // of a slot load two rounds each, a step ahead, and pass them around
     static_assert(!kWide || R <= 16, "two rounds a thread");
     struct Words {
@@ -606,10 +630,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_mma_kernel(const __grid_co
     Words raw_k, raw_v;
     // packed codes: the word is 24 bits from byte t / 4 * 3 of a row, in one or two aligned words;
     // every row and step has the same alignment (t_cap and steps are multiples of 64 tokens)
-    const unsigned shift = kWide && a.code_bits == 6 ? (3u * slot & 3u) * 8u : 0u;
+    const unsigned shift = kWide && a.code_bits == 6 ? (3u * (slot >> 1) & 3u) * 8u : 0u;
     auto load_codes = [&](const uint8_t* codes, Words& w, int i) {
       if constexpr (kWide) {
-        const long long t = start + static_cast<long long>(i) * kGroupTok + 4 * slot;
+        const long long t = start + static_cast<long long>(i) * kGroupTok + 4 * (slot >> 1);
         const size_t row_bytes = a.code_bits == 6 ? static_cast<size_t>(a.t_cap) / 4 * 3 : static_cast<size_t>(a.t_cap);
         const uint8_t* p = codes + ((static_cast<size_t>(h) * kWideGroups + rank) * rounds + cl) * row_bytes +
                            (a.code_bits == 6 ? t / 4 * 3 - (shift >> 3) : t);
@@ -638,7 +662,27 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_mma_kernel(const __grid_co
     };
     // offset of the codeword of word w and token u within a round of a codebook
     const int unit = a.code_bits == 6 ? 6 : 8;
-    auto entry = [&](uint32_t w, int u) { return ((w >> (unit * u)) & 63u) * 128u; };
+    const int first_bit = (slot & 1) * kPer * unit;
+    auto entry = [&](uint32_t w, int u) { return ((w >> (first_bit + unit * u)) & 63u) * 128u; };
+    // the codewords of all rounds, summed: neighbouring rounds in fp16 (rounded once more), those
+    // sums in fp32
+    auto sum_rounds = [&](float (&x)[kPer][8], uint32_t book, const uint32_t (&w)[kWide ? R : 1]) {
+#pragma unroll
+      for (int u = 0; u < kPer; ++u)
+#pragma unroll
+        for (int d = 0; d < 8; ++d) x[u][d] = 0.f;
+#pragma unroll
+      for (int r = 0; r < (kWide ? R : 0); r += 2) {
+        if (r >= rounds) continue;
+        const bool both = r + 1 < R && r + 1 < rounds;
+#pragma unroll
+        for (int u = 0; u < kPer; ++u) {
+          uint4 y = lds16(book + r * (kWideCodes * 128) + entry(w[r], u));
+          if (both) y = add_chunks(y, lds16(book + (r + 1) * (kWideCodes * 128) + entry(w[r + 1 < R ? r + 1 : 0], u)));
+          add_chunk(x[u], y);
+        }
+      }
+    };
     // Keys of step i + 2 and values of step i: keys run two steps ahead, so that the softmax of a
     // tile runs under the making of its values; the two are interleaved, so that the gathers of
     // one run under the arithmetic of the other.
@@ -648,7 +692,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_mma_kernel(const __grid_co
       const int sk = ik & 1, sv = kVStages == 2 ? i & 1 : 0, lap = i / kVStages;
       const uint32_t tile_k = tiles_k + sk * kTile, tile_v = tiles_v + sv * kTile;
       const long long left = end - (start + static_cast<long long>(i) * kGroupTok);       // of the values' step
-      uint4 v[4];
+      uint4 v[kPer];
       if (keys && ik % kReanchor == 0 && ik > 0) anchor(ik);
       auto keys_free = [&] { return ik < 2 || wait(&ctl.k_empty[sk], ((ik >> 1) - 1) & 1, a.fault); };
       if constexpr (kWide) {
@@ -656,23 +700,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_mma_kernel(const __grid_co
           uint32_t wk[R];
           share_codes(raw_k, wk);
           if (!keys_free()) return false;
-#pragma unroll
-          for (int u = 0; u < 4; u += 2) {
-            float x[2][8];
-#pragma unroll
-            for (int d = 0; d < 8; ++d) x[0][d] = x[1][d] = 0.f;
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-              if (r < rounds) {
-                add_chunk(x[0], lds16(my_k + r * (kWideCodes * 128) + entry(wk[r], u)));
-                add_chunk(x[1], lds16(my_k + r * (kWideCodes * 128) + entry(wk[r], u + 1)));
-              }
-            }
+          float x[kPer][8];
+          sum_rounds(x, my_k, wk);
+          {
+            constexpr int u = 0;
             store(tile_k, u, ph.rotate(x[0]), &ctl.k_full[sk]);
             ph.turn(step);
             store(tile_k, u + 1, ph.rotate(x[1]), &ctl.k_full[sk]);
-            if (u == 0) ph.turn(step);
-            else ph.turn(jump);
+            ph.turn(jump);
           }
           publish(&ctl.k_full[sk]);
           if (ik + 1 < ntiles) load_codes(a.key_codes, raw_k, ik + 1);
@@ -680,36 +715,25 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_mma_kernel(const __grid_co
         if (values) {
           uint32_t wv[R];
           share_codes(raw_v, wv);
+          float x[kPer][8];
+          sum_rounds(x, my_v, wv);
 #pragma unroll
-          for (int u = 0; u < 4; u += 2) {
-            float x[2][8];
-#pragma unroll
-            for (int d = 0; d < 8; ++d) x[0][d] = x[1][d] = 0.f;
-#pragma unroll
-            for (int r = 0; r < R; ++r) {
-              if (r < rounds) {
-                add_chunk(x[0], lds16(my_v + r * (kWideCodes * 128) + entry(wv[r], u)));
-                add_chunk(x[1], lds16(my_v + r * (kWideCodes * 128) + entry(wv[r], u + 1)));
-              }
-            }
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-              v[u + k] = make_uint4(half_pair(x[k][0], x[k][1]), half_pair(x[k][2], x[k][3]), half_pair(x[k][4], x[k][5]),
-                                    half_pair(x[k][6], x[k][7]));
-          }
+          for (int u = 0; u < kPer; ++u)
+            v[u] = make_uint4(half_pair(x[u][0], x[u][1]), half_pair(x[u][2], x[u][3]), half_pair(x[u][4], x[u][5]),
+                              half_pair(x[u][6], x[u][7]));
           if (i + 1 < ntiles) load_codes(a.val_codes, raw_v, i + 1);
         }
       } else {
-        uint32_t wk[4 * R], wv[4 * R];
+        uint32_t wk[kPer * R], wv[kPer * R];
         if (values) {
           if (!wait(&ctl.c_full[1][i % kCodeStages], (i / kCodeStages) & 1, a.fault)) return false;
 #pragma unroll
-          for (int j = 0; j < 4 * R; ++j) wv[j] = code(i, kCodeBytes, j / R, j % R);
+          for (int j = 0; j < kPer * R; ++j) wv[j] = code(i, kCodeBytes, j / R, j % R);
         }
         auto gather_values = [&] {
           if (!values) return;
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
+          for (int u = 0; u < kPer; ++u) {
             v[u] = lds16(my_v + wv[u * R] * (CH * 16));
 #pragma unroll
             for (int r = 1; r < R; ++r) {
@@ -721,14 +745,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_mma_kernel(const __grid_co
         if (keys) {
           if (!wait(&ctl.c_full[0][ik % kCodeStages], (ik / kCodeStages) & 1, a.fault)) return false;
 #pragma unroll
-          for (int j = 0; j < 4 * R; ++j) wk[j] = code(ik, 0, j / R, j % R);
-          uint4 k[4 * R];
+          for (int j = 0; j < kPer * R; ++j) wk[j] = code(ik, 0, j / R, j % R);
+          uint4 k[kPer * R];
 #pragma unroll
-          for (int j = 0; j < 4 * R; ++j) k[j] = lds16(my_k + (j % R) * (kCodes * CH * 16) + wk[j] * (CH * 16));
+          for (int j = 0; j < kPer * R; ++j) k[j] = lds16(my_k + (j % R) * (kCodes * CH * 16) + wk[j] * (CH * 16));
           if (R == 1) gather_values();
           if (!keys_free()) return false;
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
+          for (int u = 0; u < kPer; ++u) {
 #pragma unroll
             for (int r = 1; r < R; ++r) k[u * R] = add_chunks(k[u * R], k[u * R + r]);
             store(tile_k, u, ph.rotate(k[u * R]), &ctl.k_full[sk]);
@@ -745,11 +769,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefix_mma_kernel(const __grid_co
       if (lap > 0 && !wait(&ctl.v_empty[sv], (lap - 1) & 1, a.fault)) return false;
       if (left < kGroupTok) {
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
+        for (int u = 0; u < kPer; ++u)
           if (token(u) >= left) v[u] = make_uint4(0u, 0u, 0u, 0u);          // weight 0 times this must be 0
       }
 #pragma unroll
-      for (int u = 0; u < 4; ++u) store(tile_v, u, v[u], &ctl.v_full[sv]);
+      for (int u = 0; u < kPer; ++u) store(tile_v, u, v[u], &ctl.v_full[sv]);
       publish(&ctl.v_full[sv]);
       if (!kWide && lane == 0) arrive(&ctl.c_empty[1][i % kCodeStages]);
       return true;
@@ -936,7 +960,7 @@ cudaError_t run(const ServeArgs& a, cudaStream_t stream) {
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.n_splits * C, a.n_kv_heads, (a.batch * a.group + kRows - 1) / kRows);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(Roles<kWide>::kThreads);
   cfg.dynamicSmemBytes = bytes;
   cfg.stream = stream;
   cfg.attrs = attr;
