@@ -4,8 +4,8 @@
 //
 // A CTA takes 128 query rows ((sequence, head of the group) pairs) of a KV head and a run of
 // tokens, in tiles of 64:
-//   producers            gather codewords from fp16 codebooks in shared memory, sum the
-//                        rounds, rotate the keys and store key and value tiles
+//   producers (8 warps for keys, 4 or 8 for values)  gather codewords from fp16 codebooks in
+//                        shared memory, sum the rounds, rotate the keys and store the tiles
 //   one thread           copies codes, steps ahead, into shared memory (8-scalar groups)
 //   two threads          S = Q K^T (M = 128 rows, N = 64 tokens; Q from TMEM), O += P V
 //                        (N = 128 dims; P from TMEM), both tcgen05.mma kind::f16
@@ -31,6 +31,8 @@
 // each), sums of rounds and everything after the products stay in fp32, except that two value
 // codewords (8-scalar groups) are added as fp16: that sum would be rounded to fp16 next anyhow.
 // Codebooks are scaled by a power of two into fp16's range, and so is each query row.
+#include <type_traits>
+
 #include "serve.cuh"
 
 namespace cvq {
@@ -38,13 +40,12 @@ namespace cvq {
 namespace {
 
 constexpr int kSoftWarps = 8;
-// The warps by their roles.  Eight producer warps for 8-scalar groups; the many gathers of a
-// 64-scalar group want sixteen, in fewer registers each.
+// The warps by their roles.
 template <bool kWide>
 struct Roles {
-  static constexpr int kProdWarps = kWide ? 16 : 8;
-  static constexpr int kProd = 32 * kProdWarps;
-  static constexpr int kScoreWarp = kSoftWarps + kProdWarps, kOutWarp = kScoreWarp + 1, kCopyWarp = kOutWarp + 1;
+  static constexpr int kKeyWarps = 8, kValueWarps = kWide ? 8 : 4;
+  static constexpr int kValueWarp = kSoftWarps + kKeyWarps;                   // the first
+  static constexpr int kScoreWarp = kValueWarp + kValueWarps, kOutWarp = kScoreWarp + 1, kCopyWarp = kOutWarp + 1;
   static constexpr int kThreads = 32 * (kCopyWarp + 1);
 };
 constexpr int kRows = 128;
@@ -348,15 +349,11 @@ __device__ __forceinline__ float2 query_pair(uint32_t w, bool bf16) {
 template <int C, bool kWide, int R>
 __global__ void __launch_bounds__(Roles<kWide>::kThreads, 1) prefix_mma_kernel(const __grid_constant__ ServeArgs a) {
   using W = Roles<kWide>;
-  constexpr int kProdWarps = W::kProdWarps, kProd = W::kProd, kThreads = W::kThreads;
-  constexpr int kScoreWarp = W::kScoreWarp, kCopyWarp = W::kCopyWarp;
+  constexpr int kThreads = W::kThreads, kScoreWarp = W::kScoreWarp, kCopyWarp = W::kCopyWarp;
   constexpr int kGroupTok = C * kTok;             // tokens of a step of the CTA or pair
   constexpr int CH = 16 / C;
-  constexpr int kSlots = kProd / CH;              // tokens that the producers take at once
-  constexpr int kPer = kGroupTok / kSlots;        // tokens of a producer thread in a step
   constexpr int kVStages = kWide ? 1 : 2;
   constexpr int kCodeStages = kMostCodeStages / C;
-  static_assert(kPer * kSlots == kGroupTok && kPer == (kWide ? 2 : 4), "the code below");
   static_assert(!kWide || C == 2, "a CTA holds one 64-scalar group");
   extern __shared__ __align__(1024) unsigned char smem[];
   const uint32_t tiles_k = smem_u32(smem), tiles_v = tiles_k + 2 * kTile;
@@ -407,8 +404,8 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, 1) prefix_mma_kernel(c
     mbar_init(&ctl.q_full, nact);
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&ctl.k_full[s], kProdWarps);
-      mbar_init(&ctl.v_full[s], kProdWarps);
+      mbar_init(&ctl.k_full[s], W::kKeyWarps);
+      mbar_init(&ctl.v_full[s], W::kValueWarps);
       mbar_init(&ctl.k_empty[s], C);
       mbar_init(&ctl.v_empty[s], C);
       mbar_init(&ctl.s_full[s], 1);
@@ -421,7 +418,7 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, 1) prefix_mma_kernel(c
 #pragma unroll
       for (int v = 0; v < 2; ++v) {
         mbar_init(&ctl.c_full[v][s], 1);
-        mbar_init(&ctl.c_empty[v][s], kProdWarps);
+        mbar_init(&ctl.c_empty[v][s], v ? W::kValueWarps : W::kKeyWarps);
       }
     }
   }
@@ -504,7 +501,7 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, 1) prefix_mma_kernel(c
         if (!wait(&ctl.s_full[st], par, a.fault)) break;
         tmem_after_sync();
         // 64 scores, held at once where the registers allow it and else read twice
-        constexpr int kHeld = kWide ? 1 : 2;
+        constexpr int kHeld = 1;
         const long long left = end - (start + static_cast<long long>(i) * kGroupTok + rank * kTok);
         uint32_t s[kHeld][32];
         auto load_scores = [&](int c, uint32_t (&x)[32]) {
@@ -583,220 +580,183 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, 1) prefix_mma_kernel(c
       tmem_after_sync();
     }
     if (m != -INFINITY) m -= kLift;
-  } else if (warp < kSoftWarps + kProdWarps) {
+  } else if (warp < kScoreWarp) {
     // ================= producers =================
-    const int tid = threadIdx.x - 32 * kSoftWarps;
-    const int cl = tid % CH, slot = tid / CH;
-    const int chunk = C == 2 ? 8 * rank + cl : cl;
-    // token u of this thread within a step, the CTA it belongs to and its row of the tile there
-    auto token = [&](int u) { return kWide ? kPer * slot + u : slot + u * kSlots; };
-    uint32_t at[kPer];                            // of its 16 bytes, from the start of a tile
-    bool mine[kPer];
-#pragma unroll
-    for (int u = 0; u < kPer; ++u) {
-      const int row = token(u) % kTok, to = C == 2 ? token(u) / kTok : 0;
-      mine[u] = to == rank;
-      at[u] = (chunk >> 3) * kHalfTile + row * 128 + (((chunk & 7) ^ (row & 7)) << 4);
-      if (!mine[u]) at[u] += C == 2 ? map_to(tiles_k, static_cast<uint32_t>(to)) - tiles_k : 0;
-    }
-    const uint32_t away = C == 2 ? map_to(tiles_k, static_cast<uint32_t>(rank ^ 1)) - tiles_k : 0;
-    auto store = [&](uint32_t tile, int u, uint4 v, uint64_t* bar) {
-      if (C == 1 || mine[u]) sts16(tile + at[u], v);
-      else send16(tile + at[u], v, smem_u32(bar) + away);
-    };
-    // a stage is full when this CTA's warps have stored and the other CTA's half has landed
-    auto publish = [&](uint64_t* bar) {
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        if (C == 2 && warp == kSoftWarps) mbar_expect_tx(bar, kHalfTile);
-        else arrive(bar);
+    // Keys and values are made by warps of their own.
+    auto produce = [&](auto is_keys) {
+      constexpr bool kKeys = decltype(is_keys)::value;
+      constexpr int kWarps = kKeys ? W::kKeyWarps : W::kValueWarps, kFirst = kKeys ? kSoftWarps : W::kValueWarp;
+      constexpr int kSlots = 32 * kWarps / CH;    // tokens taken at once
+      constexpr int kPer = kGroupTok / kSlots;    // tokens of a thread in a step
+      constexpr int kStages = kKeys ? 2 : kVStages;
+      static_assert(!kWide || kPer == 4, "a word of codes is 4 tokens");
+      static_assert(kWide || kSlots % 8 == 0, "the rows of a thread have the same swizzle");
+      const int tid = threadIdx.x - 32 * kFirst, cl = tid % CH, slot = tid / CH;
+      const int chunk = C == 2 ? 8 * rank + cl : cl;
+      uint64_t* full = kKeys ? ctl.k_full : ctl.v_full;
+      uint64_t* empty = kKeys ? ctl.k_empty : ctl.v_empty;
+      const uint32_t tiles = kKeys ? tiles_k : tiles_v, book = (kKeys ? cb_k : cb_v) + cl * 16;
+      const uint8_t* codes = kKeys ? a.key_codes : a.val_codes;
+      // Token u of this thread within a step, and its 16 bytes' place in a tile of its CTA: row
+      // token % 64 of CTA token / 64.
+      auto token = [&](int u) { return kWide ? kPer * slot + u : slot + u * kSlots; };
+      const int row = token(0) % kTok;
+      const uint32_t at0 = (chunk >> 3) * kHalfTile + row * 128, swizzle = (chunk & 7) ^ (row & 7);
+      const uint32_t away = C == 2 ? map_to(tiles_k, static_cast<uint32_t>(rank ^ 1)) - tiles_k : 0;
+      auto store = [&](int s, int u, uint4 v) {
+        const uint32_t at = tiles + s * kTile + at0 + (kWide ? u * 128 + ((swizzle ^ u) << 4) : (u * kSlots % kTok) * 128 + (swizzle << 4));
+        const int to = kWide ? slot / (kTok / kPer) : u * kSlots / kTok;
+        if (C == 1 || to == rank) sts16(at, v);
+        else send16(at + away, v, smem_u32(full + s) + away);
+      };
+      // a stage is full when this CTA's warps have stored and the other CTA's half has landed
+      auto publish = [&](int s) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          if (C == 2 && warp == kFirst) mbar_expect_tx(full + s, kHalfTile);
+          else arrive(full + s);
+        }
+      };
+      Phase ph, step, jump;
+      auto anchor = [&](int i) {
+        ph.set(a.phase, chunk, static_cast<unsigned long long>(start + static_cast<long long>(i) * kGroupTok + token(0)));
+      };
+      if (kKeys) {
+        step.set(a.phase, chunk, kWide ? 1 : kSlots);
+        if (kWide) jump.set(a.phase, chunk, kGroupTok - (kPer - 1));
+        anchor(0);
       }
-    };
-    Phase ph, step, jump;
-    step.set(a.phase, chunk, kWide ? 1 : kSlots);
-    if (kWide) jump.set(a.phase, chunk, kGroupTok - (kPer - 1));
-    auto anchor = [&](int i) {
-      ph.set(a.phase, chunk, static_cast<unsigned long long>(start + static_cast<long long>(i) * kGroupTok + token(0)));
-    };
-    anchor(0);
-    const uint32_t my_k = cb_k + cl * 16, my_v = cb_v + cl * 16;
-    // 64-scalar groups: a word holds the codes of 4 tokens, two slots', for a round; the 8 threads
-    // of a slot load two rounds each, a step ahead, and pass them around
-    static_assert(!kWide || R <= 16, "two rounds a thread");
-    struct Words {
+      // 64-scalar groups: a word holds the codes of this slot's 4 tokens for a round; the 8 threads
+      // of a slot load two rounds each, a step ahead, and pass them around.  Packed codes: the word
+      // is 24 bits from byte t / 4 * 3 of a row, in one or two aligned words; every row and step
+      // has the same alignment (t_cap and steps are multiples of 64 tokens)
+      static_assert(!kWide || R <= 16, "two rounds a thread");
       uint32_t lo[2], hi[2];
-    };
-    Words raw_k, raw_v;
-    // packed codes: the word is 24 bits from byte t / 4 * 3 of a row, in one or two aligned words;
-    // every row and step has the same alignment (t_cap and steps are multiples of 64 tokens)
-    const unsigned shift = kWide && a.code_bits == 6 ? (3u * (slot >> 1) & 3u) * 8u : 0u;
-    auto load_codes = [&](const uint8_t* codes, Words& w, int i) {
-      if constexpr (kWide) {
-        const long long t = start + static_cast<long long>(i) * kGroupTok + 4 * (slot >> 1);
+      const unsigned shift = kWide && a.code_bits == 6 ? (3u * slot & 3u) * 8u : 0u;
+      auto load_words = [&](int i) {
+        const long long t = start + static_cast<long long>(i) * kGroupTok + 4 * slot;
         const size_t row_bytes = a.code_bits == 6 ? static_cast<size_t>(a.t_cap) / 4 * 3 : static_cast<size_t>(a.t_cap);
         const uint8_t* p = codes + ((static_cast<size_t>(h) * kWideGroups + rank) * rounds + cl) * row_bytes +
                            (a.code_bits == 6 ? t / 4 * 3 - (shift >> 3) : t);
 #pragma unroll
         for (int k = 0; k < 2; ++k, p += 8 * row_bytes) {
-          w.lo[k] = w.hi[k] = 0u;
+          lo[k] = hi[k] = 0u;
           if (cl + 8 * k < rounds && t < end) {
-            w.lo[k] = __ldg(reinterpret_cast<const uint32_t*>(p));
-            if (shift > 8) w.hi[k] = __ldg(reinterpret_cast<const uint32_t*>(p) + 1);
+            lo[k] = __ldg(reinterpret_cast<const uint32_t*>(p));
+            if (shift > 8) hi[k] = __ldg(reinterpret_cast<const uint32_t*>(p) + 1);
           }
         }
-      }
-    };
-    auto share_codes = [&](const Words& w, uint32_t (&of)[kWide ? R : 1]) {
-      const uint32_t w0 = __funnelshift_r(w.lo[0], w.hi[0], shift), w1 = __funnelshift_r(w.lo[1], w.hi[1], shift);
-#pragma unroll
-      for (int r = 0; r < (kWide ? R : 1); ++r) of[r] = __shfl_sync(0xffffffffu, r < 8 ? w0 : w1, (lane & 24) | (r & 7));
-    };
-    // 8-scalar groups: codes from the ring (behind the last token any byte, all of them entries)
-    const uint32_t my_codes = ring + token(0) * (R * kGroups) + chunk;
-    auto code = [&](int i, uint32_t values, int u, int r) {
-      uint32_t x;
-      asm volatile("ld.shared.u8 %0, [%1];" : "=r"(x)
-                   : "r"(my_codes + (i % kCodeStages) * (2 * kCodeBytes) + values + u * (kSlots * R * kGroups) + r * kGroups));
-      return x;
-    };
-    // offset of the codeword of word w and token u within a round of a codebook
-    const int unit = a.code_bits == 6 ? 6 : 8;
-    const int first_bit = (slot & 1) * kPer * unit;
-    auto entry = [&](uint32_t w, int u) { return ((w >> (first_bit + unit * u)) & 63u) * 128u; };
-    // the codewords of all rounds, summed: neighbouring rounds in fp16 (rounded once more), those
-    // sums in fp32
-    auto sum_rounds = [&](float (&x)[kPer][8], uint32_t book, const uint32_t (&w)[kWide ? R : 1]) {
-#pragma unroll
-      for (int u = 0; u < kPer; ++u)
-#pragma unroll
-        for (int d = 0; d < 8; ++d) x[u][d] = 0.f;
-#pragma unroll
-      for (int r = 0; r < (kWide ? R : 0); r += 2) {
-        if (r >= rounds) continue;
-        const bool both = r + 1 < R && r + 1 < rounds;
-#pragma unroll
-        for (int u = 0; u < kPer; ++u) {
-          uint4 y = lds16(book + r * (kWideCodes * 128) + entry(w[r], u));
-          if (both) y = add_chunks(y, lds16(book + (r + 1) * (kWideCodes * 128) + entry(w[r + 1 < R ? r + 1 : 0], u)));
-          add_chunk(x[u], y);
+      };
+      // offset of the codeword of word w and token u within a round of a codebook
+      const int unit = a.code_bits == 6 ? 6 : 8;
+      auto entry = [&](uint32_t w, int u) { return ((w >> (unit * u)) & 63u) * 128u; };
+      // 8-scalar groups: codes from the ring (behind the last token any byte, all of them entries)
+      const uint32_t my_codes = ring + (kKeys ? 0 : kCodeBytes) + token(0) * (R * kGroups) + chunk;
+      auto code = [&](int i, int u, int r) {
+        uint32_t x;
+        asm volatile("ld.shared.u8 %0, [%1];" : "=r"(x)
+                     : "r"(my_codes + (i % kCodeStages) * (2 * kCodeBytes) + u * (kSlots * R * kGroups) + r * kGroups));
+        return x;
+      };
+      if (kWide) load_words(0);
+      asm volatile("griddepcontrol.wait;" ::: "memory");
+      const int e = book_exponent(kKeys ? 0 : 1);
+      wait(&ctl.book, 0, a.fault);
+      if (e != kUsualScale) {                     // far from the usual size: scaled anew, from the codebook itself
+        const float* cb = kKeys ? a.key_cb + static_cast<long long>(h) * a.key_cb_stride
+                                : a.val_cb + static_cast<long long>(h) * a.val_cb_stride;
+        for (int i = tid; i < book_items<C, kWide>(rounds); i += 32 * kWarps) {
+          const float4* x = reinterpret_cast<const float4*>(book_item<C, kWide>(cb, rounds, rank, i));
+          sts16((kKeys ? cb_k : cb_v) + i * 16, scaled_halves(__ldg(x), __ldg(x + 1), ldexpf(1.f, e), kKeys));
         }
+        asm volatile("bar.sync %0, %1;" ::"n"(kKeys ? 1 : 2), "n"(32 * kWarps) : "memory");
       }
-    };
-    // Keys of step i + 2 and values of step i: keys run two steps ahead, so that the softmax of a
-    // tile runs under the making of its values; the two are interleaved, so that the gathers of
-    // one run under the arithmetic of the other.
-    auto make = [&](int i) {
-      const int ik = i + 2;
-      const bool keys = ik < ntiles, values = i >= 0;
-      const int sk = ik & 1, sv = kVStages == 2 ? i & 1 : 0, lap = i / kVStages;
-      const uint32_t tile_k = tiles_k + sk * kTile, tile_v = tiles_v + sv * kTile;
-      const long long left = end - (start + static_cast<long long>(i) * kGroupTok);       // of the values' step
-      uint4 v[kPer];
-      if (keys && ik % kReanchor == 0 && ik > 0) anchor(ik);
-      auto keys_free = [&] { return ik < 2 || wait(&ctl.k_empty[sk], ((ik >> 1) - 1) & 1, a.fault); };
-      if constexpr (kWide) {
-        if (keys) {
-          uint32_t wk[R];
-          share_codes(raw_k, wk);
-          if (!keys_free()) return false;
-          float x[kPer][8];
-          sum_rounds(x, my_k, wk);
+      for (int i = 0; i < ntiles; ++i) {
+        const int s = kStages == 2 ? i & 1 : 0, lap = i / kStages;
+        auto stage_free = [&] { return lap == 0 || wait(empty + s, (lap - 1) & 1, a.fault); };
+        const long long left = end - (start + static_cast<long long>(i) * kGroupTok);
+        if (kKeys && i % kReanchor == 0 && i > 0) anchor(i);
+        if constexpr (kWide) {
+          uint32_t w[R];
           {
-            constexpr int u = 0;
-            store(tile_k, u, ph.rotate(x[0]), &ctl.k_full[sk]);
-            ph.turn(step);
-            store(tile_k, u + 1, ph.rotate(x[1]), &ctl.k_full[sk]);
-            ph.turn(jump);
+            const uint32_t w0 = __funnelshift_r(lo[0], hi[0], shift), w1 = __funnelshift_r(lo[1], hi[1], shift);
+#pragma unroll
+            for (int r = 0; r < R; ++r) w[r] = __shfl_sync(0xffffffffu, r < 8 ? w0 : w1, (lane & 24) | (r & 7));
           }
-          publish(&ctl.k_full[sk]);
-          if (ik + 1 < ntiles) load_codes(a.key_codes, raw_k, ik + 1);
-        }
-        if (values) {
-          uint32_t wv[R];
-          share_codes(raw_v, wv);
-          float x[kPer][8];
-          sum_rounds(x, my_v, wv);
+          if (i + 1 < ntiles) load_words(i + 1);
+          if (!stage_free()) break;
 #pragma unroll
-          for (int u = 0; u < kPer; ++u)
-            v[u] = make_uint4(half_pair(x[u][0], x[u][1]), half_pair(x[u][2], x[u][3]), half_pair(x[u][4], x[u][5]),
-                              half_pair(x[u][6], x[u][7]));
-          if (i + 1 < ntiles) load_codes(a.val_codes, raw_v, i + 1);
-        }
-      } else {
-        uint32_t wk[kPer * R], wv[kPer * R];
-        if (values) {
-          if (!wait(&ctl.c_full[1][i % kCodeStages], (i / kCodeStages) & 1, a.fault)) return false;
+          for (int u0 = 0; u0 < kPer; u0 += 2) {
+            // the codewords of all rounds, summed: neighbouring rounds in fp16 (rounded once
+            // more), those sums in fp32
+            float x[2][8];
 #pragma unroll
-          for (int j = 0; j < kPer * R; ++j) wv[j] = code(i, kCodeBytes, j / R, j % R);
-        }
-        auto gather_values = [&] {
-          if (!values) return;
+            for (int u = 0; u < 2; ++u)
 #pragma unroll
-          for (int u = 0; u < kPer; ++u) {
-            v[u] = lds16(my_v + wv[u * R] * (CH * 16));
+              for (int d = 0; d < 8; ++d) x[u][d] = 0.f;
 #pragma unroll
-            for (int r = 1; r < R; ++r) {
-              const uint4 y = lds16(my_v + r * (kCodes * CH * 16) + wv[u * R + r] * (CH * 16));
-              v[u] = add_chunks(v[u], y);
+            for (int r = 0; r < R; r += 2) {
+              if (r >= rounds) continue;
+              const bool both = r + 1 < R && r + 1 < rounds;
+#pragma unroll
+              for (int u = 0; u < 2; ++u) {
+                uint4 y = lds16(book + r * (kWideCodes * 128) + entry(w[r], u0 + u));
+                if (both) y = add_chunks(y, lds16(book + (r + 1) * (kWideCodes * 128) + entry(w[r + 1 < R ? r + 1 : 0], u0 + u)));
+                add_chunk(x[u], y);
+              }
+            }
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              if (kKeys) {
+                store(s, u0 + u, ph.rotate(x[u]));
+                if (u0 + u < kPer - 1) ph.turn(step);
+                else ph.turn(jump);
+              } else {
+                uint4 v = make_uint4(half_pair(x[u][0], x[u][1]), half_pair(x[u][2], x[u][3]), half_pair(x[u][4], x[u][5]),
+                                     half_pair(x[u][6], x[u][7]));
+                if (token(u0 + u) >= left) v = make_uint4(0u, 0u, 0u, 0u);  // weight 0 times this must be 0
+                store(s, u0 + u, v);
+              }
             }
           }
-        };
-        if (keys) {
-          if (!wait(&ctl.c_full[0][ik % kCodeStages], (ik / kCodeStages) & 1, a.fault)) return false;
-#pragma unroll
-          for (int j = 0; j < kPer * R; ++j) wk[j] = code(ik, 0, j / R, j % R);
-          uint4 k[kPer * R];
-#pragma unroll
-          for (int j = 0; j < kPer * R; ++j) k[j] = lds16(my_k + (j % R) * (kCodes * CH * 16) + wk[j] * (CH * 16));
-          if (R == 1) gather_values();
-          if (!keys_free()) return false;
-#pragma unroll
-          for (int u = 0; u < kPer; ++u) {
-#pragma unroll
-            for (int r = 1; r < R; ++r) k[u * R] = add_chunks(k[u * R], k[u * R + r]);
-            store(tile_k, u, ph.rotate(k[u * R]), &ctl.k_full[sk]);
-            ph.turn(step);
-            if (R > 1 && u == 1) gather_values();
-          }
-          publish(&ctl.k_full[sk]);
-          if (lane == 0) arrive(&ctl.c_empty[0][ik % kCodeStages]);          // publish joined the warp
         } else {
-          gather_values();
+          uint64_t* c_full = &ctl.c_full[kKeys ? 0 : 1][i % kCodeStages];
+          if (!wait(c_full, (i / kCodeStages) & 1, a.fault)) break;
+          uint32_t w[kPer * R];
+#pragma unroll
+          for (int j = 0; j < kPer * R; ++j) w[j] = code(i, j / R, j % R);
+          constexpr int kBatch = kPer < 4 ? kPer : 4;                        // gathers in flight
+          bool ok = true;
+#pragma unroll
+          for (int u0 = 0; u0 < kPer; u0 += kBatch) {
+            uint4 v[kBatch * R];
+#pragma unroll
+            for (int j = 0; j < kBatch * R; ++j) v[j] = lds16(book + (j % R) * (kCodes * CH * 16) + w[u0 * R + j] * (CH * 16));
+            if (u0 == 0) ok = stage_free();
+            if (!ok) break;
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+              uint4 x = v[u * R];
+#pragma unroll
+              for (int r = 1; r < R; ++r) x = add_chunks(x, v[u * R + r]);
+              if (kKeys) {
+                x = ph.rotate(x);
+                ph.turn(step);
+              } else if (left < kGroupTok && token(u0 + u) >= left) {
+                x = make_uint4(0u, 0u, 0u, 0u);
+              }
+              store(s, u0 + u, x);
+            }
+          }
+          if (!ok) break;
         }
+        publish(s);
+        if (!kWide && lane == 0) arrive(&ctl.c_empty[kKeys ? 0 : 1][i % kCodeStages]);
       }
-      if (!values) return true;
-      if (lap > 0 && !wait(&ctl.v_empty[sv], (lap - 1) & 1, a.fault)) return false;
-      if (left < kGroupTok) {
-#pragma unroll
-        for (int u = 0; u < kPer; ++u)
-          if (token(u) >= left) v[u] = make_uint4(0u, 0u, 0u, 0u);          // weight 0 times this must be 0
-      }
-#pragma unroll
-      for (int u = 0; u < kPer; ++u) store(tile_v, u, v[u], &ctl.v_full[sv]);
-      publish(&ctl.v_full[sv]);
-      if (!kWide && lane == 0) arrive(&ctl.c_empty[1][i % kCodeStages]);
-      return true;
     };
-    load_codes(a.key_codes, raw_k, 0);
-    load_codes(a.val_codes, raw_v, 0);
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int ek = book_exponent(0), ev = book_exponent(1);
-    wait(&ctl.book, 0, a.fault);
-    if (ek != kUsualScale || ev != kUsualScale) {
-      // far from the usual size: scaled anew, from the codebooks themselves
-      const float* kcb = a.key_cb + static_cast<long long>(h) * a.key_cb_stride;
-      const float* vcb = a.val_cb + static_cast<long long>(h) * a.val_cb_stride;
-      for (int i = tid; i < book_items<C, kWide>(rounds); i += kProd) {
-        const float4* k = reinterpret_cast<const float4*>(book_item<C, kWide>(kcb, rounds, rank, i));
-        const float4* v = reinterpret_cast<const float4*>(book_item<C, kWide>(vcb, rounds, rank, i));
-        sts16(cb_k + i * 16, scaled_halves(__ldg(k), __ldg(k + 1), ldexpf(1.f, ek), true));
-        sts16(cb_v + i * 16, scaled_halves(__ldg(v), __ldg(v + 1), ldexpf(1.f, ev), false));
-      }
-      asm volatile("bar.sync 1, %0;" ::"n"(kProd) : "memory");
-    }
-    for (int i = -2; i < ntiles; ++i)
-      if (!make(i)) break;
+    if (warp < W::kValueWarp) produce(std::true_type{});
+    else produce(std::false_type{});
   } else if (warp == kCopyWarp) {
     // ================= codes =================
     if (lane == 0) {
