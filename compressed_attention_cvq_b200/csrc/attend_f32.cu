@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(kThreads) attend_f32_kernel(const __grid_const
 // Merge of the partial states of a row (m in log2 units): a CTA per (sequence, query head), the
 // states strided over its warps, 4 dims a lane and U states in flight; the warps' sums are joined
 // in their order.  It is launched while the attention kernel still runs and waits for its end.
-constexpr int kMergeWarps = 4;
+constexpr int kMergeWarps = 8;
 __global__ void __launch_bounds__(32 * kMergeWarps) merge_kernel(const __grid_constant__ ServeArgs a) {
   __shared__ float s_m[kMergeWarps], s_l[kMergeWarps];
   __shared__ float4 s_o[kMergeWarps][32];

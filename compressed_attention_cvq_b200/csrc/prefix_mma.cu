@@ -65,7 +65,6 @@ struct Control {
   uint64_t c_full[2][kMostCodeStages], c_empty[2][kMostCodeStages];         // codes of keys, values
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], s_empty[2], p_full[2], pv_done[2];
   uint32_t tmem;
-  int q_exponent[kRows];
   float m[kRows], l[kRows];                       // second stream's state
 };
 
@@ -133,13 +132,8 @@ __device__ __forceinline__ void tmem_store32(uint32_t at, const uint32_t (&r)[32
       "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::CVQ_V4(r, 0), CVQ_V4(r, 4), CVQ_V4(r, 8), CVQ_V4(r, 12),
       CVQ_V4(r, 16), CVQ_V4(r, 20), CVQ_V4(r, 24), CVQ_V4(r, 28), "r"(at) : "memory");
 }
-// 16 rows x 64 columns: repetition j holds columns 8 j + 2 (lane % 4), + 1 of rows lane / 4 and
-// lane / 4 + 8
-__device__ __forceinline__ void tmem_store_rows(uint32_t at, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.16x256b.x8.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
-      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::CVQ_V4(r, 0), CVQ_V4(r, 4), CVQ_V4(r, 8), CVQ_V4(r, 12),
-      CVQ_V4(r, 16), CVQ_V4(r, 20), CVQ_V4(r, 24), CVQ_V4(r, 28), "r"(at) : "memory");
+__device__ __forceinline__ void tmem_store8(uint32_t at, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::CVQ_V4(r, 0), CVQ_V4(r, 4), "r"(at) : "memory");
 }
 __device__ __forceinline__ void tmem_load_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -201,6 +195,9 @@ __device__ __forceinline__ float exp2_fast(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// 2^e for -126 <= e <= 127, and floor(log2 x) of a normal number
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+__device__ __forceinline__ int log2_floor(float x) { return static_cast<int>(__float_as_uint(x) >> 23 & 255) - 127; }
 __device__ __forceinline__ uint32_t half_pair(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -227,11 +224,13 @@ __device__ __forceinline__ uint4 add_chunks(uint4 x, uint4 y) {
 struct Phase {
   f2 c[2], s[2];
   __device__ __forceinline__ void set(const PhaseTurns& ph, int chunk, unsigned long long t) {
+    float2 v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = phase_exact(ph.F[4 * chunk + j] * t);
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
-      const float2 x = phase_exact(ph.F[4 * chunk + 2 * p] * t), y = phase_exact(ph.F[4 * chunk + 2 * p + 1] * t);
-      c[p] = pack(x.x, y.x);
-      s[p] = pack(x.y, y.y);
+      c[p] = pack(v[2 * p].x, v[2 * p + 1].x);
+      s[p] = pack(v[2 * p].y, v[2 * p + 1].y);
     }
   }
   __device__ __forceinline__ void turn(const Phase& w) {
@@ -337,7 +336,7 @@ __global__ void __launch_bounds__(kBookThreads) prefix_book_kernel(const __grid_
 __device__ __forceinline__ int scale_exponent(uint32_t peak_bits, int R) {
   const float most = __uint_as_float(peak_bits) * static_cast<float>(R) * 1.5f;      // 1.5 > sqrt 2: rotated
   if (peak_bits == 0 || (most < 512.f && most > 0.0078125f)) return kUsualScale;
-  return min(max(14 - ilogbf(fminf(most, 3e38f)), -120), 120);
+  return min(max(14 - log2_floor(most), -114), 120);
 }
 
 // two 16-bit query elements as floats
@@ -401,7 +400,7 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, 1) prefix_mma_kernel(c
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   } else if (warp == kCopyWarp && lane == 0) {
     mbar_init(&ctl.book, 1);
-    mbar_init(&ctl.q_full, nact);
+    mbar_init(&ctl.q_full, 2 * nact);
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       mbar_init(&ctl.k_full[s], W::kKeyWarps);
@@ -428,14 +427,18 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, 1) prefix_mma_kernel(c
   else __syncthreads();
   tmem_after_sync();
   constexpr uint32_t tmem = 0;                    // all columns: the allocation starts at 0
-  // scale exponent of the key (0) or value (1) codebook of this KV head; after the wait for
+  // scale exponents of the key and value codebooks of this KV head; after the wait for
   // prefix_book_kernel
-  auto book_exponent = [&](int values) {
+  auto book_exponents = [&] {
     const int n = C * book_items<C, kWide>(rounds) / kBookThreads;
-    const uint32_t* at = a.book_peak + (static_cast<size_t>(h) * 2 + values) * n;
-    uint32_t peak = 0;
-    for (int i = lane; i < n; i += 32) peak = max(peak, __ldcg(at + i));
-    return scale_exponent(__reduce_max_sync(0xffffffffu, peak), rounds);
+    const uint32_t* at = a.book_peak + static_cast<size_t>(h) * 2 * n;
+    uint32_t k = 0, v = 0;
+#pragma unroll 1
+    for (int i = lane; i < n; i += 32) {
+      k = max(k, __ldcg(at + i));
+      v = max(v, __ldcg(at + n + i));
+    }
+    return make_int2(scale_exponent(__reduce_max_sync(0xffffffffu, k), rounds), scale_exponent(__reduce_max_sync(0xffffffffu, v), rounds));
   };
 
   float m = -INFINITY, l = 0.f;                   // softmax: log2 maximum and sum of this thread's row
@@ -448,43 +451,46 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, 1) prefix_mma_kernel(c
     // rescaled a few times and not at every tile, and weights stay below 2^(kLift + kSlack)
     constexpr float kLift = 7.f, kSlack = 8.f;
     if (q4 < nact) {
-      if (st == 0) {
-        // the query operand: 16 rows at a time, 4 lanes a row with 4 elements of every 16 each,
-        // the largest of a row brought to [2^8, 2^9)
+      // the query operand: the largest element of a row brought to [2^8, 2^9); each stream stores
+      // half of the dims.  The loops are rolled: code that runs once costs more to fetch than to run
+      int eq;
+      {
+        const int r = q4 * 32 + lane;
         const bool bf16 = a.q_dtype == CVQ_BF16;
+        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + global_row(min(r, nrows - 1)) * kHeadDim);
+        float mx = 0.f;
 #pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
-          uint32_t x[32];
+        for (int i = 0; i < 4; ++i) {
+          uint4 v[4];
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int r = q4 * 32 + 16 * half + 8 * k + (lane >> 2);
-            const uint2* src = reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.q) + global_row(min(r, nrows - 1)) * kHeadDim) + (lane & 3);
-            float mx = 0.f;
+          for (int k = 0; k < 4; ++k) v[k] = __ldg(src + 4 * i + k);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const uint2 v = __ldg(src + 4 * j);
-              x[4 * j + 2 * k] = v.x;
-              x[4 * j + 2 * k + 1] = v.y;
-            }
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const float2 f = query_pair(x[4 * (j >> 1) + 2 * k + (j & 1)], bf16);
+            for (int j = 0; j < 4; ++j) {
+              const float2 f = query_pair(w[j], bf16);
               mx = fmaxf(mx, fmaxf(fabsf(f.x), fabsf(f.y)));
             }
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-            const int eq = mx > 0.f && mx < INFINITY ? 8 - ilogbf(mx) : 0;
-            if ((lane & 3) == 0) ctl.q_exponent[r] = eq;
-            const float up = ldexpf(1.f, min(eq, 127)), rest = ldexpf(1.f, eq - min(eq, 127));
+          }
+        }
+        eq = mx > 0.f && mx < INFINITY ? 8 - log2_floor(mx) : 0;
+        const float up = r < nrows ? pow2(min(eq, 127)) : 0.f, rest = pow2(eq - min(eq, 127));
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) {             // 16 dims: 8 columns
+          const uint4 v[2] = {__ldg(src + 8 * st + 2 * i), __ldg(src + 8 * st + 2 * i + 1)};
+          uint32_t x[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              uint32_t &w0 = x[4 * j + 2 * k], &w1 = x[4 * j + 2 * k + 1];
-              const float2 f0 = query_pair(w0, bf16), f1 = query_pair(w1, bf16);
-              w0 = r < nrows ? half_pair(f0.x * up * rest, f1.x * up * rest) : 0u;      // in the keys' order
-              w1 = r < nrows ? half_pair(f0.y * up * rest, f1.y * up * rest) : 0u;
+          for (int k = 0; k < 2; ++k) {
+            const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+            for (int j = 0; j < 4; j += 2) {
+              const float2 f0 = query_pair(w[j], bf16), f1 = query_pair(w[j + 1], bf16);
+              x[4 * k + j] = half_pair(f0.x * up * rest, f1.x * up * rest);            // in the keys' order
+              x[4 * k + j + 1] = half_pair(f0.y * up * rest, f1.y * up * rest);
             }
           }
-          tmem_store_rows(lanes + (static_cast<uint32_t>(16 * half) << 16) + kColQ, x);
+          tmem_store8(lanes + kColQ + 32 * st + 8 * i, x);
         }
         tmem_store_wait();
         tmem_before_sync();
@@ -492,16 +498,16 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, 1) prefix_mma_kernel(c
         if (lane == 0) arrive(&ctl.q_full);
       }
       asm volatile("griddepcontrol.wait;" ::: "memory");
-      const int ek = book_exponent(0);
-      ev = book_exponent(1);
-      wait(&ctl.q_full, 0, a.fault);
-      const float factor = ldexpf(0.08838834764831845f * kLog2e, -ctl.q_exponent[q4 * 32 + lane] - ek);
+      const int2 e = book_exponents();
+      ev = e.y;
+      const int by = min(max(-eq - e.x, -252), 252);
+      const float factor = 0.08838834764831845f * kLog2e * pow2(by / 2) * pow2(by - by / 2);
       for (int i = st; i < ntiles; i += 2) {
         const unsigned par = (i >> 1) & 1;
         if (!wait(&ctl.s_full[st], par, a.fault)) break;
         tmem_after_sync();
         // 64 scores, held at once where the registers allow it and else read twice
-        constexpr int kHeld = 1;
+        constexpr int kHeld = kWide ? 1 : 2;
         const long long left = end - (start + static_cast<long long>(i) * kGroupTok + rank * kTok);
         uint32_t s[kHeld][32];
         auto load_scores = [&](int c, uint32_t (&x)[32]) {
@@ -661,14 +667,15 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, 1) prefix_mma_kernel(c
       };
       if (kWide) load_words(0);
       asm volatile("griddepcontrol.wait;" ::: "memory");
-      const int e = book_exponent(kKeys ? 0 : 1);
+      const int2 both = book_exponents();
+      const int e = kKeys ? both.x : both.y;
       wait(&ctl.book, 0, a.fault);
       if (e != kUsualScale) {                     // far from the usual size: scaled anew, from the codebook itself
         const float* cb = kKeys ? a.key_cb + static_cast<long long>(h) * a.key_cb_stride
                                 : a.val_cb + static_cast<long long>(h) * a.val_cb_stride;
         for (int i = tid; i < book_items<C, kWide>(rounds); i += 32 * kWarps) {
           const float4* x = reinterpret_cast<const float4*>(book_item<C, kWide>(cb, rounds, rank, i));
-          sts16((kKeys ? cb_k : cb_v) + i * 16, scaled_halves(__ldg(x), __ldg(x + 1), ldexpf(1.f, e), kKeys));
+          sts16((kKeys ? cb_k : cb_v) + i * 16, scaled_halves(__ldg(x), __ldg(x + 1), pow2(e), kKeys));
         }
         asm volatile("bar.sync %0, %1;" ::"n"(kKeys ? 1 : 2), "n"(32 * kWarps) : "memory");
       }
@@ -861,7 +868,7 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, 1) prefix_mma_kernel(c
     const float m1 = second ? ctl.m[r] : -INFINITY, l1 = second ? ctl.l[r] : 0.f;
     const float M = fmaxf(m, m1), ref = M == -INFINITY ? 0.f : M;
     const float f0 = exp2f(m - ref), f1 = exp2f(m1 - ref);
-    const float back = ldexpf(1.f, -ev);
+    const float back = pow2(-ev);
 #pragma unroll 1
     for (int c = 0; c < 4; ++c) {
       uint32_t o[32];
