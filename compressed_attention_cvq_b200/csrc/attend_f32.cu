@@ -23,49 +23,94 @@ __device__ __forceinline__ int wide_code(const uint8_t* codes, const ServeArgs& 
   return codes[row * a.t_cap + t] & 63;
 }
 
-// 8 dims (chunk c) of the key and value of token t of KV head h, decoded from the codes; the
-// key rotated by position t
-__device__ __forceinline__ void decode_chunk(const ServeArgs& a, const unsigned long long* f_tab, int h, int t,
-                                             int c, float (&k)[8], float (&v)[8]) {
-#pragma unroll
-  for (int d = 0; d < 8; ++d) k[d] = v[d] = 0.f;
+__device__ __forceinline__ void add8(float (&x)[8], const float* p) {
+  const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  x[0] += a.x; x[1] += a.y; x[2] += a.z; x[3] += a.w;
+  x[4] += b.x; x[5] += b.y; x[6] += b.z; x[7] += b.w;
+}
+__device__ __forceinline__ void put8(float* at, const float (&x)[8]) {
+  reinterpret_cast<float4*>(at)[0] = make_float4(x[0], x[1], x[2], x[3]);
+  reinterpret_cast<float4*>(at)[1] = make_float4(x[4], x[5], x[6], x[7]);
+}
+
+// A tile of keys and values, decoded, the keys rotated by their positions.  A thread makes chunk
+// c = tid % 16 (8 dims) of kPer tokens, all of whose codes it loads before the first codeword and
+// all of whose codewords before the first sum (8-scalar groups, kR rounds; 64-scalar groups,
+// kR = 0, go round by round).  Tokens from `end` on are zeros.
+template <int kR>
+__device__ __forceinline__ void make_tile(const ServeArgs& a, const unsigned long long* f_tab, int h, int t0, int end,
+                                          float* sk, float* sv) {
+  constexpr int kPer = kTile * 16 / kThreads, kStep = kThreads / 16;
+  const int c = threadIdx.x & 15, tk = threadIdx.x >> 4;
   const float* kcb = a.key_cb + h * a.key_cb_stride;
   const float* vcb = a.val_cb + h * a.val_cb_stride;
-  for (int r = 0; r < a.R; ++r) {
-    size_t ko, vo;
-    if (a.wide) {
-      const int G = c >> 3;
-      const size_t base = (static_cast<size_t>(G) * a.R + r) * kWideCodes;
-      ko = (base + wide_code(a.key_codes, a, h, G, r, t)) * kWideGroupDim + 8 * (c & 7);
-      vo = (base + wide_code(a.val_codes, a, h, G, r, t)) * kWideGroupDim + 8 * (c & 7);
-    } else {
-      const size_t row = ((static_cast<size_t>(h) * a.t_cap + t) * a.R + r) * kGroups + c;
-      const size_t base = (static_cast<size_t>(c) * a.R + r) * kCodes;
-      ko = (base + a.key_codes[row]) * kCodeword;
-      vo = (base + a.val_codes[row]) * kVDims;
+  float k[kPer][8], v[kPer][8];
+#pragma unroll
+  for (int u = 0; u < kPer; ++u)
+#pragma unroll
+    for (int d = 0; d < 8; ++d) k[u][d] = v[u][d] = 0.f;
+  if constexpr (kR > 0) {
+    int kc[kPer * kR], vc[kPer * kR];
+#pragma unroll
+    for (int j = 0; j < kPer * kR; ++j) {
+      const int t = min(t0 + tk + j / kR * kStep, end - 1);
+      const size_t row = ((static_cast<size_t>(h) * a.t_cap + t) * kR + j % kR) * kGroups + c;
+      kc[j] = __ldg(a.key_codes + row);
+      vc[j] = __ldg(a.val_codes + row);
     }
-    const float4 a0 = __ldg(reinterpret_cast<const float4*>(kcb + ko));
-    const float4 a1 = __ldg(reinterpret_cast<const float4*>(kcb + ko) + 1);
-    const float4 b0 = __ldg(reinterpret_cast<const float4*>(vcb + vo));
-    const float4 b1 = __ldg(reinterpret_cast<const float4*>(vcb + vo) + 1);
-    k[0] += a0.x; k[1] += a0.y; k[2] += a0.z; k[3] += a0.w;
-    k[4] += a1.x; k[5] += a1.y; k[6] += a1.z; k[7] += a1.w;
-    v[0] += b0.x; v[1] += b0.y; v[2] += b0.z; v[3] += b0.w;
-    v[4] += b1.x; v[5] += b1.y; v[6] += b1.z; v[7] += b1.w;
+#pragma unroll
+    for (int j = 0; j < kPer * kR; ++j) {
+      const size_t base = (static_cast<size_t>(c) * kR + j % kR) * kCodes;
+      add8(k[j / kR], kcb + (base + kc[j]) * kCodeword);
+      add8(v[j / kR], vcb + (base + vc[j]) * kVDims);
+    }
+  } else {
+    const int G = c >> 3;
+    for (int r = 0; r < a.R; ++r) {
+      const size_t base = (static_cast<size_t>(G) * a.R + r) * kWideCodes;
+#pragma unroll
+      for (int u = 0; u < kPer; ++u) {
+        const int t = min(t0 + tk + u * kStep, end - 1);
+        add8(k[u], kcb + (base + wide_code(a.key_codes, a, h, G, r, t)) * kWideGroupDim + 8 * (c & 7));
+        add8(v[u], vcb + (base + wide_code(a.val_codes, a, h, G, r, t)) * kWideGroupDim + 8 * (c & 7));
+      }
+    }
   }
+  // phases of the first token, turned on to the others (one fp32 rounding each)
+  float2 ph[4], step[4];
 #pragma unroll
   for (int p = 0; p < 4; ++p) {
-    const float2 ph = phase_exact(f_tab[4 * c + p] * static_cast<unsigned long long>(static_cast<unsigned>(t)));
-    const float re = k[2 * p], im = k[2 * p + 1];
-    k[2 * p] = re * ph.x - im * ph.y;
-    k[2 * p + 1] = re * ph.y + im * ph.x;
+    ph[p] = phase_exact(f_tab[4 * c + p] * static_cast<unsigned long long>(static_cast<unsigned>(t0 + tk)));
+    step[p] = phase_exact(f_tab[4 * c + p] * kStep);
+  }
+#pragma unroll
+  for (int u = 0; u < kPer; ++u) {
+    const int row = tk + u * kStep;
+    if (u > 0) {
+#pragma unroll
+      for (int p = 0; p < 4; ++p)
+        ph[p] = make_float2(ph[p].x * step[p].x - ph[p].y * step[p].y, ph[p].x * step[p].y + ph[p].y * step[p].x);
+    }
+    if (t0 + row < end) {
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        const float re = k[u][2 * p], im = k[u][2 * p + 1];
+        k[u][2 * p] = re * ph[p].x - im * ph[p].y;
+        k[u][2 * p + 1] = re * ph[p].y + im * ph[p].x;
+      }
+    } else {
+#pragma unroll
+      for (int d = 0; d < 8; ++d) k[u][d] = v[u][d] = 0.f;
+    }
+    put8(sk + row * kPad + 8 * c, k[u]);
+    put8(sv + row * kHeadDim + 8 * c, v[u]);
   }
 }
 
 // RB query rows per CTA: the rows of a KV head are (sequence, head of the group) pairs, and
 // blockIdx.z takes RB of them.
 template <int RB>
-__global__ void __launch_bounds__(kThreads) attend_f32_kernel(const __grid_constant__ ServeArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) attend_f32_kernel(const __grid_constant__ ServeArgs a) {
   constexpr int RPT = RB / 16;
   extern __shared__ float4 smem4[];
   float* sq = reinterpret_cast<float*>(smem4);      // [RB][kPad]
@@ -89,12 +134,21 @@ __global__ void __launch_bounds__(kThreads) attend_f32_kernel(const __grid_const
     return static_cast<size_t>(rr / a.group) * a.n_q_heads + h * a.group + rr % a.group;
   };
   for (int i = tid; i < kPairs; i += kThreads) f_tab[i] = a.phase.F[i];
-  for (int i = tid; i < RB * kHeadDim; i += kThreads) {
+  // a query element; few rows are loaded here and stored under the first tile's gathers
+  auto query = [&](int i) {
     const int r = i / kHeadDim, d = i % kHeadDim;
-    float x = 0.f;
-    if (r0 + r < rows && start < end) x = load_any(a.q, a.q_dtype, grow(r) * kHeadDim + d);
-    sq[r * kPad + d] = x * (0.08838834764831845f * kLog2e);
+    const float x = r0 + r < rows && start < end ? load_any(a.q, a.q_dtype, grow(r) * kHeadDim + d) : 0.f;
+    return x * (0.08838834764831845f * kLog2e);
+  };
+  constexpr int kEarly = RB == 16 ? RB * kHeadDim / kThreads : 0;
+  float early[kEarly + 1];
+#pragma unroll
+  for (int u = 0; u < kEarly; ++u) early[u] = query(tid + u * kThreads);
+  if (kEarly == 0) {
+#pragma unroll 8
+    for (int i = tid; i < RB * kHeadDim; i += kThreads) sq[i / kHeadDim * kPad + i % kHeadDim] = query(i);
   }
+  __syncthreads();                                  // f_tab
   float m[RPT], l[RPT], o[RPT][8];
 #pragma unroll
   for (int i = 0; i < RPT; ++i) {
@@ -105,22 +159,15 @@ __global__ void __launch_bounds__(kThreads) attend_f32_kernel(const __grid_const
   }
   for (int t0 = start; t0 < end; t0 += kTile) {
     __syncthreads();                                // the last tile's readers are done
+    if (a.wide) make_tile<0>(a, f_tab, h, t0, end, sk, sv);
+    else if (a.R == 1) make_tile<1>(a, f_tab, h, t0, end, sk, sv);
+    else make_tile<2>(a, f_tab, h, t0, end, sk, sv);
+    if (t0 == start) {
 #pragma unroll
-    for (int u = 0; u < kTile * 16 / kThreads; ++u) {
-      const int i = tid + u * kThreads, tk = i >> 4, c = i & 15, t = t0 + tk;
-      float k[8], v[8];
-      if (t < end) {
-        decode_chunk(a, f_tab, h, t, c, k, v);
-      } else {
-#pragma unroll
-        for (int d = 0; d < 8; ++d) k[d] = v[d] = 0.f;
+      for (int u = 0; u < kEarly; ++u) {
+        const int i = tid + u * kThreads;
+        sq[i / kHeadDim * kPad + i % kHeadDim] = early[u];
       }
-      float4* kd = reinterpret_cast<float4*>(sk + tk * kPad + 8 * c);
-      kd[0] = make_float4(k[0], k[1], k[2], k[3]);
-      kd[1] = make_float4(k[4], k[5], k[6], k[7]);
-      float4* vd = reinterpret_cast<float4*>(sv + tk * kHeadDim + 8 * c);
-      vd[0] = make_float4(v[0], v[1], v[2], v[3]);
-      vd[1] = make_float4(v[4], v[5], v[6], v[7]);
     }
     __syncthreads();
     float s[RPT][4];
@@ -128,6 +175,7 @@ __global__ void __launch_bounds__(kThreads) attend_f32_kernel(const __grid_const
     for (int i = 0; i < RPT; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+#pragma unroll 4
     for (int d = 0; d < kHeadDim; d += 4) {
       float4 qv[RPT], kv[4];
 #pragma unroll
@@ -173,6 +221,7 @@ __global__ void __launch_bounds__(kThreads) attend_f32_kernel(const __grid_const
       for (int d = 0; d < 8; ++d) o[i][d] *= alpha;
     }
     __syncthreads();
+#pragma unroll 8
     for (int t = 0; t < kTile; ++t) {
       float p[RPT];
       if constexpr (RPT == 4) {

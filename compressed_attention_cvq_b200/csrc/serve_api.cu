@@ -105,10 +105,14 @@ int cvq_prefix_suggest_splits(const cvq_shape* s, int q_dtype, int sm_count) {
   if (cvq_partials_bytes(s, 1) == 0 || sm_count < 1 || !is_dtype(q_dtype)) return 1;
   const long long rows = static_cast<long long>(s->batch) * (s->n_q_heads / s->n_kv_heads);
   if (prefix_on_tensor_cores(s, q_dtype)) {
-    // one CTA per SM; a split holds a tile of each CTA
-    const long long ctas = static_cast<long long>(s->n_kv_heads) * ((rows + 127) / 128) * prefix_pair(s);
-    const long long most = (static_cast<long long>(s->t_cap) + 64 * prefix_pair(s) - 1) / (64 * prefix_pair(s));
-    return static_cast<int>(std::max(1LL, std::min({4096LL, most, sm_count / ctas})));
+    // One CTA per SM, and of pairs those that fit at once (72 on 148 SMs).  A split of single CTAs
+    // holds a tile of 64 tokens; one of pairs, which have more to set up, two of each CTA, and four
+    // beyond 16 splits (12345 tokens of 2 KV heads: 25 splits 17.4 us, 33 splits 19.0)
+    const int pair = prefix_pair(s);
+    const long long ctas = static_cast<long long>(s->n_kv_heads) * ((rows + 127) / 128) * pair;
+    const long long tiles = (static_cast<long long>(s->t_cap) + 63) / 64;
+    const long long most = pair == 1 ? tiles : std::max((tiles + 7) / 8, std::min((tiles + 3) / 4, 16LL));
+    return static_cast<int>(std::max(1LL, std::min({4096LL, most, (pair == 1 ? sm_count : sm_count - 4) / ctas})));
   }
   const long long units = s->n_kv_heads * (rows <= 16 ? 1 : (rows + 63) / 64);
   const long long tiles = std::max(1LL, (static_cast<long long>(s->t_cap) + 63) / 64);
