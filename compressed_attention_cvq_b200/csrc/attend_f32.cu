@@ -134,19 +134,40 @@ __global__ void __launch_bounds__(kThreads, 2) attend_f32_kernel(const __grid_co
     return static_cast<size_t>(rr / a.group) * a.n_q_heads + h * a.group + rr % a.group;
   };
   for (int i = tid; i < kPairs; i += kThreads) f_tab[i] = a.phase.F[i];
-  // a query element; few rows are loaded here and stored under the first tile's gathers
-  auto query = [&](int i) {
-    const int r = i / kHeadDim, d = i % kHeadDim;
-    const float x = r0 + r < rows && start < end ? load_any(a.q, a.q_dtype, grow(r) * kHeadDim + d) : 0.f;
-    return x * (0.08838834764831845f * kLog2e);
-  };
-  constexpr int kEarly = RB == 16 ? RB * kHeadDim / kThreads : 0;
-  float early[kEarly + 1];
+  // 8 elements of a query row, scaled; few rows are loaded here and stored under the first tile's
+  // gathers
+  auto query = [&](int i, float (&x)[8]) {
+    const int r = i / 16;
+    if (r0 + r >= rows || start >= end) {
 #pragma unroll
-  for (int u = 0; u < kEarly; ++u) early[u] = query(tid + u * kThreads);
-  if (kEarly == 0) {
-#pragma unroll 8
-    for (int i = tid; i < RB * kHeadDim; i += kThreads) sq[i / kHeadDim * kPad + i % kHeadDim] = query(i);
+      for (int d = 0; d < 8; ++d) x[d] = 0.f;
+      return;
+    }
+    const size_t at = grow(r) * kHeadDim + i % 16 * 8;
+    if (a.q_dtype == CVQ_F32) {
+      const float4 u = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + at));
+      const float4 v = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + at) + 1);
+      x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
+      x[4] = v.x; x[5] = v.y; x[6] = v.z; x[7] = v.w;
+    } else {
+#pragma unroll
+      for (int d = 0; d < 8; ++d) x[d] = load_any(a.q, a.q_dtype, at + d);
+    }
+  };
+  auto put_query = [&](int i, float (&x)[8]) {
+#pragma unroll
+    for (int d = 0; d < 8; ++d) x[d] *= 0.08838834764831845f * kLog2e;
+    put8(sq + i / 16 * kPad + i % 16 * 8, x);
+  };
+  float early[8];
+  if (RB == 16) {
+    query(tid, early);
+  } else {
+#pragma unroll 1
+    for (int i = tid; i < RB * 16; i += kThreads) {
+      query(i, early);
+      put_query(i, early);
+    }
   }
   __syncthreads();                                  // f_tab
   float m[RPT], l[RPT], o[RPT][8];
@@ -162,13 +183,7 @@ __global__ void __launch_bounds__(kThreads, 2) attend_f32_kernel(const __grid_co
     if (a.wide) make_tile<0>(a, f_tab, h, t0, end, sk, sv);
     else if (a.R == 1) make_tile<1>(a, f_tab, h, t0, end, sk, sv);
     else make_tile<2>(a, f_tab, h, t0, end, sk, sv);
-    if (t0 == start) {
-#pragma unroll
-      for (int u = 0; u < kEarly; ++u) {
-        const int i = tid + u * kThreads;
-        sq[i / kHeadDim * kPad + i % kHeadDim] = early[u];
-      }
-    }
+    if (RB == 16 && t0 == start) put_query(tid, early);
     __syncthreads();
     float s[RPT][4];
 #pragma unroll
