@@ -110,7 +110,7 @@ __device__ __forceinline__ void make_tile(const ServeArgs& a, const unsigned lon
 // RB query rows per CTA: the rows of a KV head are (sequence, head of the group) pairs, and
 // blockIdx.z takes RB of them.
 template <int RB>
-__global__ void __launch_bounds__(kThreads, 2) attend_f32_kernel(const __grid_constant__ ServeArgs a) {
+__global__ void __launch_bounds__(kThreads, RB == 16 ? 2 : 1) attend_f32_kernel(const __grid_constant__ ServeArgs a) {
   constexpr int RPT = RB / 16;
   extern __shared__ float4 smem4[];
   float* sq = reinterpret_cast<float*>(smem4);      // [RB][kPad]
