@@ -366,11 +366,12 @@ CVQ_API cvq_status cvq_attend_static(const cvq_shape* shape, const void* q, int 
  *              workspace must be ordered on one stream
  *   out        [B, Hq, 128] of out_dtype (fp32, bf16 or fp16), 16-byte aligned
  *   lse        [B, Hq] fp32, natural log
- *   Arithmetic: fp32 queries are multiplied in fp32.  16-bit queries are multiplied on the
- *              tensor cores as fp16: codewords, the rotated key, the summed value and the
- *              softmax weights are rounded to fp16 once each (2^-11 at most), codebooks and
- *              query rows scaled by powers of two into its range, sums kept in fp32.  More
- *              than 11 rounds (group_dim 64) are multiplied in fp32
+ *   Arithmetic: fp32 queries, caches of t_cap < 512 and more than 11 rounds (group_dim 64)
+ *              are multiplied in fp32.  The other 16-bit queries are multiplied on the tensor
+ *              cores as fp16: codewords, rounds' sums, the sines, the rotated key, the value
+ *              and the softmax weights are rounded to fp16 (2^-11 at most each), codebooks
+ *              and query rows scaled by powers of two into its range; sums of products, the
+ *              softmax and the merge are kept in fp32
  *   Errors as in cvq_attend.
  * ------------------------------------------------------------------------------- */
 CVQ_API size_t cvq_prefix_workspace_bytes(const cvq_shape* shape, int n_splits);

@@ -253,3 +253,90 @@ def test_head_offsets_past_32_bits(dtype):
     kc[:, :, :512], vc[:, :, :512] = dev["key_codes"], dev["val_codes"]
     # whole splits are empty: only the first holds the 500 tokens
     verify(d, call(cvq, dev, 500, codes=(kc, vc), n_splits=2), 500, dtype)
+
+
+@pytest.mark.parametrize("group,R,bits", [(8, 1, 0), (8, 2, 0), (64, 1, 8), (64, 4, 6), (64, 11, 8)])
+@pytest.mark.parametrize("length", [0, 1, 63, 64, 65, 127, 129, 192, 513, 640])
+def test_short_prefixes_in_a_larger_cache(group, R, bits, length):
+    """Lengths around the tiles of 64 and the pairs' steps of 128 tokens, in a cache with room for
+    640, as one split and as several."""
+    import compressed_attention_cvq_b200 as cvq
+    d, dev = make(5, 8, 2, 640, R, "fp16", group, seed=R + length)
+    codes = None
+    if bits == 6:
+        shape = cvq.shape_of(dev["q"][:1], dev["key_codes"], group_dim=64)
+        shape.code_bits = 6
+        codes = [cvq.pack_codes6(shape, dev[k]) for k in ("key_codes", "val_codes")]
+    for n in (1, 3):
+        verify(d, call(cvq, dev, length, group, bits, n, codes), length, "fp16")
+    assert cvq.fault_status(clear=True) == 0
+
+
+@pytest.mark.parametrize("B,g", [(31, 4), (32, 4), (33, 4), (128, 1), (129, 1), (32, 8), (1, 8)])
+@pytest.mark.parametrize("R", [1, 2])
+def test_row_counts_around_a_block(B, g, R):
+    """124 to 258 rows of a KV head: a block holds 128."""
+    import compressed_attention_cvq_b200 as cvq
+    d, dev = make(B, 2 * g, 2, 700, R, "bf16", seed=B + R)
+    verify(d, call(cvq, dev, 690), 690, "bf16")
+
+
+@pytest.mark.parametrize("group,R", [(8, 1), (8, 2), (64, 3), (64, 11)])
+@pytest.mark.parametrize("k_scale,v_scale", [(2.0 ** 20, 1.0), (2.0 ** -30, 2.0 ** -40), (1.0, 2.0 ** 60),
+                                             (2.0 ** 12, 2.0 ** 110)])
+def test_codebooks_far_from_one(group, R, k_scale, v_scale):
+    """Codebooks that leave fp16's range as they are; the queries take the keys' scale back."""
+    import compressed_attention_cvq_b200 as cvq
+    d, dev = make(4, 8, 2, 640, R, "bf16", group, seed=R)
+    for name, f in (("key_cb", k_scale), ("val_cb", v_scale)):
+        d[name] = (d[name] * np.float32(f)).astype(np.float32)
+        dev[name] = torch.from_numpy(d[name]).cuda()
+    dev["q"] = (dev["q"].double() / k_scale).bfloat16()
+    d["q"] = dev["q"].double().cpu().numpy()
+    got = call(cvq, dev, 600, group, out_dtype=torch.float32)
+    # measured in units of the values' scale, where the absolute terms of the tolerance belong
+    d["val_cb"] = d["val_cb"] / v_scale
+    verify(d, (got[0].double() / v_scale, got[1]), 600, "bf16", "fp32")
+
+
+def test_queries_far_from_one():
+    import compressed_attention_cvq_b200 as cvq
+    for f in (2.0 ** -100, 2.0 ** 90):
+        d, dev = make(3, 8, 2, 640, 2, "bf16", seed=2)
+        d["key_cb"] = (d["key_cb"] / np.float32(f)).astype(np.float32)
+        dev["key_cb"] = torch.from_numpy(d["key_cb"]).cuda()
+        dev["q"] = (dev["q"].double() * f).bfloat16()
+        d["q"] = dev["q"].double().cpu().numpy()
+        verify(d, call(cvq, dev, 640), 640, "bf16")
+    # a row of zeros attends evenly; a row that is not finite leaves the others alone
+    d, dev = make(3, 8, 2, 640, 2, "bf16", seed=3)
+    want = call(cvq, dev, 640)
+    dev["q"][0, 1] = 0
+    dev["q"][1, 5, 7] = float("nan")
+    dev["q"][2, 2, 9] = float("inf")
+    out, lse = call(cvq, dev, 640)
+    assert torch.allclose(lse[0, 1], torch.tensor(640.0).log().cuda(), atol=1e-6)
+    assert torch.isnan(out[1, 5]).all() and torch.isnan(lse[1, 5]) and torch.isnan(out[2, 2]).all()
+    same = torch.ones(3, 8, dtype=torch.bool)
+    same[0, 1] = same[1, 5] = same[2, 2] = False
+    assert torch.equal(out[same], want[0][same]) and torch.equal(lse[same], want[1][same])
+
+
+@pytest.mark.parametrize("R,dtype,bits", [(12, "bf16", 6), (22, "fp16", 8), (21, "fp32", 6)])
+def test_many_rounds(R, dtype, bits):
+    import compressed_attention_cvq_b200 as cvq
+    d, dev = make(6, 8, 2, 640, R, dtype, 64, seed=R)
+    codes = None
+    if bits == 6:
+        shape = cvq.shape_of(dev["q"][:1], dev["key_codes"], group_dim=64)
+        shape.code_bits = 6
+        codes = [cvq.pack_codes6(shape, dev[k]) for k in ("key_codes", "val_codes")]
+    verify(d, call(cvq, dev, 601, 64, bits, codes=codes), 601, dtype)
+
+
+def test_long_streams_keep_their_phases():
+    """A split of hundreds of tiles: the keys' turning phases are taken anew every 64 tiles."""
+    import compressed_attention_cvq_b200 as cvq
+    for R, group in ((1, 8), (2, 8), (2, 64)):
+        d, dev = make(2, 4, 1, 30016, R, "fp16", group, seed=R)
+        verify(d, call(cvq, dev, 30001, group, n_splits=1), 30001, "fp16")
