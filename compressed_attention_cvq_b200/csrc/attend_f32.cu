@@ -119,6 +119,7 @@ __global__ void __launch_bounds__(kThreads, RB == 16 ? 2 : 1) attend_f32_kernel(
   float* sp = sk;                                   // [kTile][RB], over the keys once they are read
   __shared__ unsigned long long f_tab[kPairs];
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  asm volatile("griddepcontrol.wait;" ::: "memory");                        // for what ran before this call
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");         // the merge
   const int split = blockIdx.x, h = blockIdx.y;
   const int rows = a.batch * a.group;
@@ -352,8 +353,7 @@ cudaError_t run(const ServeArgs& a, dim3 grid, cudaStream_t stream) {
   static_assert(RB <= kPad, "the weights fit over the keys");
   const cudaError_t e = set_smem_limit_once(flag, attend_f32_kernel<RB>, bytes);
   if (e != cudaSuccess) return e;
-  attend_f32_kernel<RB><<<grid, kThreads, bytes, stream>>>(a);
-  return cudaGetLastError();
+  return launch_chained(attend_f32_kernel<RB>, grid, kThreads, a, stream, bytes);
 }
 
 }  // namespace
@@ -365,16 +365,7 @@ cudaError_t launch_prefix_f32(const ServeArgs& a, cudaStream_t stream) {
 }
 
 cudaError_t launch_merge(const ServeArgs& a, cudaStream_t stream) {
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(a.batch) * a.n_q_heads);
-  cfg.blockDim = dim3(32 * kMergeWarps);
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, merge_kernel, a);
+  return launch_chained(merge_kernel, dim3(static_cast<unsigned>(a.batch) * a.n_q_heads), 32 * kMergeWarps, a, stream);
 }
 
 }  // namespace cvq

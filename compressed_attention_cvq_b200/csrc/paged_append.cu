@@ -49,6 +49,7 @@ __global__ void __launch_bounds__(kThreads, 6) paged_append_kernel(const __grid_
   const int i = blockIdx.x, c = threadIdx.x & 15, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int nq = a.q != nullptr ? a.n_q_heads : 0, nk = nq + a.n_kv_heads, heads = nk + a.n_kv_heads;   // queries, keys, values
   const int stride = gridDim.y * kSlots;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   Chunk<In> in[kRows];
   auto load = [&](int r0) {
 #pragma unroll
@@ -143,9 +144,8 @@ cudaError_t launch_in(const AppendArgs& a, int kv_dtype, cudaStream_t stream) {
   // where there are fewer tokens than make 8 CTAs an SM of 148, several CTAs share a token's rows
   const int most = (heads + kSlots - 1) / kSlots;
   const dim3 grid(a.n_tokens, std::max(1, std::min(most, 8 * 148 / a.n_tokens)));
-  if (kv_dtype == CVQ_BF16) paged_append_kernel<In, __nv_bfloat16><<<grid, kThreads, 0, stream>>>(a);
-  else paged_append_kernel<In, __half><<<grid, kThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  return kv_dtype == CVQ_BF16 ? launch_chained(paged_append_kernel<In, __nv_bfloat16>, grid, kThreads, a, stream)
+                              : launch_chained(paged_append_kernel<In, __half>, grid, kThreads, a, stream);
 }
 
 }  // namespace

@@ -112,6 +112,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attend_kernel(cons
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gid = lane >> 2, tid = lane & 3;      // fragment row (head) and column pair
   const int split = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   int L = a.lens[b];
   L = L < 0 ? 0 : (L > a.t_cap ? a.t_cap : L);
   const int used = L == 0 ? 1 : (L + a.split_tokens - 1) / a.split_tokens;   // splits that hold tokens
@@ -400,8 +401,7 @@ cudaError_t run(const ServeArgs& a, cudaStream_t stream) {
   static PerDeviceFlag flag;
   const cudaError_t e = set_smem_limit_once(flag, paged_attend_kernel<T>, kSmemBytes);
   if (e != cudaSuccess) return e;
-  paged_attend_kernel<T><<<dim3(a.n_splits, a.n_kv_heads, a.batch), kThreads, kSmemBytes, stream>>>(a);
-  return cudaGetLastError();
+  return launch_chained(paged_attend_kernel<T>, dim3(a.n_splits, a.n_kv_heads, a.batch), kThreads, a, stream, kSmemBytes);
 }
 
 }  // namespace

@@ -65,7 +65,7 @@ struct Control {
   uint64_t c_full[2][kMostCodeStages], c_empty[2][kMostCodeStages];         // codes of keys, values
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], s_empty[2], p_full[2], pv_done[2];
   uint32_t tmem;
-  float m[kRows], l[kRows];                       // second stream's state
+  float m[2][kRows], l[2][kRows];                 // the streams' states
 };
 
 // ---- PTX ----
@@ -307,6 +307,7 @@ constexpr int kBookThreads = 256;
 // kernel, whose own set-up runs under it.
 template <int C, bool kWide>
 __global__ void __launch_bounds__(kBookThreads) prefix_book_kernel(const __grid_constant__ ServeArgs a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");                        // for what ran before this call
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   __shared__ uint32_t warp_peak[kBookThreads / 32];
   const int n = book_items<C, kWide>(a.R), i = blockIdx.x * kBookThreads + threadIdx.x;
@@ -847,45 +848,50 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, 1) prefix_mma_kernel(c
   __syncthreads();                                // tiles and codebooks are no longer read
 
   // ---- join the two streams and write this CTA's partial state ----
+  // Stream st finishes the dims 64 st .. 64 st + 63 and leaves its others to the other stream.
   float* rows_out = reinterpret_cast<float*>(smem);
-  const int r = (warp & 3) * 32 + lane;
-  const bool second = ntiles > 1;
-  if (second && warp >= 4 && warp < kSoftWarps && (warp & 3) < nact) {
-    ctl.m[r] = m;
-    ctl.l[r] = l;
+  const int st = warp >> 2, r = (warp & 3) * 32 + lane;
+  const bool joins = warp < kSoftWarps && (warp & 3) < nact, have = st == 0 || ntiles > 1;
+  const uint32_t out_cols = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + kColO + (st & 1) * kHeadDim;
+  if (joins) {
+    ctl.m[st][r] = m;
+    ctl.l[st][r] = l;
 #pragma unroll 1
-    for (int c = 0; c < 4; ++c) {
+    for (int c = 64 * (1 - st); c < 64 * (2 - st); c += 32) {
       uint32_t o[32];
-      tmem_load32(o, tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + kColO + kHeadDim + 32 * c);
+      tmem_load32(o, out_cols + c);
       tmem_load_wait();
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        *reinterpret_cast<uint4*>(rows_out + r * kOutPitch + 32 * c + 4 * j) = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+      for (int j = 0; j < 32; j += 4)
+        *reinterpret_cast<uint4*>(rows_out + r * kOutPitch + c + j) =
+            have ? make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]) : make_uint4(0u, 0u, 0u, 0u);
     }
   }
   __syncthreads();
-  if (warp < nact) {
-    const float m1 = second ? ctl.m[r] : -INFINITY, l1 = second ? ctl.l[r] : 0.f;
+  if (joins) {
+    const float m1 = ctl.m[1 - st][r], l1 = ctl.l[1 - st][r];
     const float M = fmaxf(m, m1), ref = M == -INFINITY ? 0.f : M;
-    const float f0 = exp2f(m - ref), f1 = exp2f(m1 - ref);
-    const float back = pow2(-ev);
+    const float back = pow2(-ev), f0 = exp2f(m - ref), f1 = exp2f(m1 - ref);
 #pragma unroll 1
-    for (int c = 0; c < 4; ++c) {
+    for (int c = 64 * st; c < 64 * (st + 1); c += 32) {
       uint32_t o[32];
-      tmem_load32(o, tmem + (static_cast<uint32_t>(warp * 32) << 16) + kColO + 32 * c);
+      tmem_load32(o, out_cols + c);
       tmem_load_wait();
 #pragma unroll
       for (int j = 0; j < 32; j += 4) {
-        float4* at = reinterpret_cast<float4*>(rows_out + r * kOutPitch + 32 * c + j);
-        float4 x = second ? *at : make_float4(0.f, 0.f, 0.f, 0.f);
-        x.x = fmaf(__uint_as_float(o[j]), f0, x.x * f1) * back;
-        x.y = fmaf(__uint_as_float(o[j + 1]), f0, x.y * f1) * back;
-        x.z = fmaf(__uint_as_float(o[j + 2]), f0, x.z * f1) * back;
-        x.w = fmaf(__uint_as_float(o[j + 3]), f0, x.w * f1) * back;
-        *at = x;
+        float4* at = reinterpret_cast<float4*>(rows_out + r * kOutPitch + c + j);
+        float4 x = *at;
+        x = make_float4(x.x * f1, x.y * f1, x.z * f1, x.w * f1);
+        if (have) {
+          x.x = fmaf(__uint_as_float(o[j]), f0, x.x);
+          x.y = fmaf(__uint_as_float(o[j + 1]), f0, x.y);
+          x.z = fmaf(__uint_as_float(o[j + 2]), f0, x.z);
+          x.w = fmaf(__uint_as_float(o[j + 3]), f0, x.w);
+        }
+        *at = make_float4(x.x * back, x.y * back, x.z * back, x.w * back);
       }
     }
-    if (r < nrows) {
+    if (st == 0 && r < nrows) {
       const size_t at = global_row(r) * n_parts + blockIdx.x;
       a.part_m[at] = M;
       a.part_l[at] = fmaf(l, f0, l1 * f1);
@@ -912,8 +918,7 @@ cudaError_t run(const ServeArgs& a, cudaStream_t stream) {
   static_assert(kMost <= 227 * 1024, "fits an SM");
   cudaError_t e = set_smem_limit_once(flag, prefix_mma_kernel<C, kWide, R>, kMost);
   if (e != cudaSuccess) return e;
-  prefix_book_kernel<C, kWide><<<dim3(book_items<C, kWide>(a.R) / kBookThreads, 2 * C, a.n_kv_heads), kBookThreads, 0, stream>>>(a);
-  e = cudaGetLastError();
+  e = launch_chained(prefix_book_kernel<C, kWide>, dim3(book_items<C, kWide>(a.R) / kBookThreads, 2 * C, a.n_kv_heads), kBookThreads, a, stream);
   if (e != cudaSuccess) return e;
   size_t bytes = kTiles + 32 * static_cast<size_t>(book_items<C, kWide>(a.R)) + kCodes8;
   if (bytes < kOutBytes) bytes = kOutBytes;

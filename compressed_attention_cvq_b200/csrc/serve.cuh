@@ -99,6 +99,23 @@ __device__ __forceinline__ float2 phase_exact(unsigned long long turn64) {
   return make_float2(c, s);
 }
 
+// A launch that may begin while the kernel before it in the stream ends; the kernel waits
+// (griddepcontrol.wait) before it touches memory.
+template <typename Args>
+cudaError_t launch_chained(void (*kernel)(const Args), dim3 grid, int threads, const Args& a, cudaStream_t stream, size_t smem = 0) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
 // the checks of cvq_shape and of a codebook head stride (api.cu)
 cvq_status check_shape_status(const cvq_shape* s);
 cvq_status check_codebook_stride(const cvq_shape* s, int64_t stride);
