@@ -15,7 +15,7 @@
 // into fp16's range, and the weights are taken relative to 2^15 below the maximum, so that the
 // small ones stay normal numbers.  Scores, weights' sums and outputs accumulate in fp32.
 //
-// Split: a CTA of 4 warps takes one (sequence, KV head, run of split_tokens tokens); a warp
+// Split: a CTA of 4 warps takes one (sequence, KV head, run of tokens); a warp
 // takes every fourth chunk of 16 tokens through its own ring of cp.async stages (keys and
 // values of a chunk, 8 KB), so that no CTA barrier runs in the loop, and keeps its own
 // maximum, sum and output; the four are joined through shared memory at the end.  A CTA whose
@@ -29,6 +29,7 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
+constexpr int kMinSplit = 256;                    // tokens that are worth a CTA and its part of a merge
 constexpr int kChunk = 16;                        // tokens of a stage
 constexpr int kStages = 3;                        // two in flight; 2, 4 and 5 measured slower
 constexpr int kRowBytes = 2 * kHeadDim;
@@ -115,10 +116,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attend_kernel(cons
   asm volatile("griddepcontrol.wait;" ::: "memory");
   int L = a.lens[b];
   L = L < 0 ? 0 : (L > a.t_cap ? a.t_cap : L);
-  const int used = L == 0 ? 1 : (L + a.split_tokens - 1) / a.split_tokens;   // splits that hold tokens
+  // the sequence's own length is split, whatever the page table has room for
+  const long long share = (L + a.n_splits - 1LL) / a.n_splits;
+  const int per = static_cast<int>(max(static_cast<long long>(kMinSplit), (share + kSplitAlign - 1) / kSplitAlign * kSplitAlign));
+  const int used = L == 0 ? 1 : static_cast<int>((L + per - 1LL) / per);     // splits that hold tokens
   if (split >= used) return;
-  const int start = split * a.split_tokens;
-  const int end = min(L - start, a.split_tokens) + start;
+  const int start = split * per;                  // < L
+  const int end = min(L - start, per) + start;
   const int nchunks = (end - start + kChunk - 1) / kChunk;
   const size_t row0 = static_cast<size_t>(b) * a.n_q_heads + static_cast<size_t>(h) * a.group;
 

@@ -18,7 +18,7 @@ struct ServeArgs {
   const void* q;
   int q_dtype;
   int batch, n_q_heads, n_kv_heads, group;
-  int n_splits, split_tokens;
+  int n_splits;
   int n_parts;                    // partial states per row: n_splits, or one per CTA of its pairs
   float* part_o;
   float* part_m;

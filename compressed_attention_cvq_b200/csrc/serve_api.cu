@@ -287,7 +287,6 @@ cvq_status cvq_paged_attend(const cvq_paged* p, const void* q, int q_dtype, cons
   a.group = p->n_q_heads / p->n_kv_heads;
   a.n_splits = a.n_parts = n_splits;
   a.t_cap = p->max_pages * p->page_size;
-  a.split_tokens = split_tokens_host(a.t_cap, n_splits);
   a.lens = seq_lens;
   a.prev_out = prev_out;
   a.prev_lse = prev_lse;

@@ -434,3 +434,57 @@ def test_streams_and_graphs(graphs):
     torch.cuda.synchronize()
     for o in outs:
         assert torch.equal(o[0], want[0]) and torch.equal(o[1], want[1])
+
+
+def test_short_sequences_in_a_wide_table():
+    """A page table with room for 64K tokens and sequences of a few: every split count of the
+    capacity's rule serves them, and the split follows the sequence."""
+    import compressed_attention_cvq_b200 as cvq
+    lens = [700, 0, 257, 64, 1025]
+    a = setup(lens, 8, 2, 16, "bf16", "bf16", seed=21, width=4096)
+    for n in (None, 1, 4, 300):
+        verify(cvq.paged_attend(*a, n), *a[1:], "bf16", "bf16")
+
+
+@pytest.mark.parametrize("call", ["append", "attend", "prefix", "prefix fp32"])
+def test_captured_behind_a_copy_a_memset_and_a_join(call):
+    """The kernels are launched under the end of whatever comes before them in the stream: in a
+    graph also behind a copy, a memset and another stream, whose results they must see."""
+    import compressed_attention_cvq_b200 as cvq
+    if call == "append":
+        pg, q, k, v, off, lens, table, kp, vp = append_case([3, 40], [5, 0], 8, 2, 16, "bf16", "bf16", 1)
+        x, run = q, lambda: cvq.paged_append(pg, k, v, off, lens, table, kp, vp, q=q)
+    elif call == "attend":
+        a = setup([300, 50], 8, 2, 16, "bf16", "bf16", seed=3)
+        x = a[1]
+        ws = cvq.paged_workspace_alloc(a[0], 4, "cuda")
+        run = lambda: cvq.paged_attend(*a, 4, workspace=ws)[0]                     # noqa: E731
+    else:
+        d = workloads.small(batch=1, n_q_heads=8, n_kv_heads=2, t_cap=640, R=2, seed=4)
+        dev = {n: torch.from_numpy(d[n]).cuda() for n in ("key_cb", "val_cb", "key_codes", "val_codes")}
+        x = torch.randn(4, 8, 128, device="cuda").to(torch.float32 if "fp32" in call else torch.bfloat16)
+        shape, ln = cvq.shape_of(x, dev["key_codes"]), i32([600])
+        n = cvq.prefix_suggest_splits(shape, x.dtype)
+        ws = cvq.prefix_workspace_alloc(shape, n, "cuda")
+        run = lambda: cvq.prefix_attend(shape, x, dev["key_cb"], dev["key_codes"],  # noqa: E731
+                                        dev["val_codes"], ln, dev["val_cb"], n, workspace=ws)[0]
+    keep = x.clone()
+    want = run().clone()
+    other = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        x.zero_()                                            # a memset or a kernel
+        other.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(other):
+            x[:1].copy_(keep[:1])
+        x[1:].copy_(keep[1:])                                # copies on both branches
+        torch.cuda.current_stream().wait_stream(other)
+        got = run()
+        after = got.clone()
+    for _ in range(3):
+        x.fill_(7)
+        g.replay()
+        torch.cuda.synchronize()
+        n = slice(None) if call != "append" else slice(0, 43)
+        assert torch.equal(got[n], want[n]) and torch.equal(after[n], want[n])
