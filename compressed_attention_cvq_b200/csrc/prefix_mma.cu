@@ -65,6 +65,7 @@ struct Control {
   uint64_t c_full[2][kMostCodeStages], c_empty[2][kMostCodeStages];         // codes of keys, values
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], s_empty[2], p_full[2], pv_done[2];
   uint32_t tmem;
+  alignas(16) float turn[16][8];                  // steps (and jumps) of the phases, per chunk
   float m[2][kRows], l[2][kRows];                 // the streams' states
 };
 
@@ -126,11 +127,13 @@ __device__ __forceinline__ void tmem_load32(uint32_t (&r)[32], uint32_t at) {
       : CVQ_R4(r, 0), CVQ_R4(r, 4), CVQ_R4(r, 8), CVQ_R4(r, 12), CVQ_R4(r, 16), CVQ_R4(r, 20), CVQ_R4(r, 24), CVQ_R4(r, 28)
       : "r"(at) : "memory");
 }
-__device__ __forceinline__ void tmem_store32(uint32_t at, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
-      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::CVQ_V4(r, 0), CVQ_V4(r, 4), CVQ_V4(r, 8), CVQ_V4(r, 12),
-      CVQ_V4(r, 16), CVQ_V4(r, 20), CVQ_V4(r, 24), CVQ_V4(r, 28), "r"(at) : "memory");
+__device__ __forceinline__ void tmem_load16(uint32_t (&r)[16], uint32_t at) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+               : CVQ_R4(r, 0), CVQ_R4(r, 4), CVQ_R4(r, 8), CVQ_R4(r, 12) : "r"(at) : "memory");
+}
+__device__ __forceinline__ void tmem_store16(uint32_t at, const uint32_t (&r)[16]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::CVQ_V4(r, 0),
+               CVQ_V4(r, 4), CVQ_V4(r, 8), CVQ_V4(r, 12), "r"(at) : "memory");
 }
 __device__ __forceinline__ void tmem_store8(uint32_t at, const uint32_t (&r)[8]) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::CVQ_V4(r, 0), CVQ_V4(r, 4), "r"(at) : "memory");
@@ -232,6 +235,19 @@ struct Phase {
       c[p] = pack(v[2 * p].x, v[2 * p + 1].x);
       s[p] = pack(v[2 * p].y, v[2 * p + 1].y);
     }
+  }
+  // 8 floats in shared memory: the 4 cosines, then the 4 sines
+  __device__ __forceinline__ void put(uint32_t at) const {
+    const float2 c0 = unpack(c[0]), c1 = unpack(c[1]), s0 = unpack(s[0]), s1 = unpack(s[1]);
+    sts16(at, make_uint4(__float_as_uint(c0.x), __float_as_uint(c0.y), __float_as_uint(c1.x), __float_as_uint(c1.y)));
+    sts16(at + 16, make_uint4(__float_as_uint(s0.x), __float_as_uint(s0.y), __float_as_uint(s1.x), __float_as_uint(s1.y)));
+  }
+  __device__ __forceinline__ void get(uint32_t at) {
+    const uint4 x = lds16(at), y = lds16(at + 16);
+    c[0] = pack(__uint_as_float(x.x), __uint_as_float(x.y));
+    c[1] = pack(__uint_as_float(x.z), __uint_as_float(x.w));
+    s[0] = pack(__uint_as_float(y.x), __uint_as_float(y.y));
+    s[1] = pack(__uint_as_float(y.z), __uint_as_float(y.w));
   }
   __device__ __forceinline__ void turn(const Phase& w) {
 #pragma unroll
@@ -541,41 +557,41 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, 1) prefix_mma_kernel(c
         if (grow) m = mx;
         const float ref = m == -INFINITY ? 0.f : m - kLift;
         const f2 ff = pack(factor, factor), rr = pack(-ref, -ref);
+        if (i >= 2) {                             // the last weights of this stream have been used
+          if (!wait(&ctl.pv_done[st], par ^ 1, a.fault)) break;
+          tmem_after_sync();
+          if (__any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll 1
+            for (int c = 0; c < kHeadDim; c += 16) {
+              uint32_t o[16];
+              tmem_load16(o, lanes + kColO + st * kHeadDim + c);
+              tmem_load_wait();
+#pragma unroll
+              for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
+              tmem_store16(lanes + kColO + st * kHeadDim + c, o);
+            }
+          }
+        }
         f2 sum = 0;
-        uint32_t p[32];
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           if (kHeld == 1 && c == 1) {
             load_scores(1, s[0]);
             scores_read();
           }
+          uint32_t p[16];
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
             const uint32_t(&x)[32] = s[c % kHeld];
             const float2 y = unpack(fma2(pack(__uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1])), ff, rr));
             const float e0 = exp2_fast(y.x), e1 = exp2_fast(y.y);
             sum = add2(sum, pack(e0, e1));
-            p[16 * c + j] = half_pair(e0, e1);
+            p[j] = half_pair(e0, e1);
           }
+          tmem_store16(lanes + kColP + st * 32 + 16 * c, p);
         }
         const float2 sums = unpack(sum);
         l = fmaf(l, alpha, sums.x + sums.y);
-        if (i >= 2) {
-          if (!wait(&ctl.pv_done[st], par ^ 1, a.fault)) break;
-          tmem_after_sync();
-          if (__any_sync(0xffffffffu, alpha != 1.f)) {
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              uint32_t o[32];
-              tmem_load32(o, lanes + kColO + st * kHeadDim + 32 * c);
-              tmem_load_wait();
-#pragma unroll
-              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
-              tmem_store32(lanes + kColO + st * kHeadDim + 32 * c, o);
-            }
-          }
-        }
-        tmem_store32(lanes + kColP + st * 32, p);
         tmem_store_wait();
         tmem_before_sync();
         __syncwarp();
@@ -625,13 +641,18 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, 1) prefix_mma_kernel(c
           else arrive(full + s);
         }
       };
-      Phase ph, step, jump;
+      // phases: this thread's own in registers, what they turn by from token to token and from
+      // step to step in shared memory, where a chunk's threads share it
+      Phase ph;
+      const uint32_t steps = smem_u32(&ctl.turn[cl][0]), jumps = steps + 8 * 32;
       auto anchor = [&](int i) {
         ph.set(a.phase, chunk, static_cast<unsigned long long>(start + static_cast<long long>(i) * kGroupTok + token(0)));
       };
       if (kKeys) {
-        step.set(a.phase, chunk, kWide ? 1 : kSlots);
-        if (kWide) jump.set(a.phase, chunk, kGroupTok - (kPer - 1));
+        if (slot == 0 || (kWide && slot == 1)) {
+          ph.set(a.phase, chunk, !kWide ? kSlots : slot == 0 ? 1 : kGroupTok - (kPer - 1));
+          ph.put(slot == 0 ? steps : jumps);
+        }
         anchor(0);
       }
       // 64-scalar groups: a word holds the codes of this slot's 4 tokens for a round; the 8 threads
@@ -667,6 +688,7 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, 1) prefix_mma_kernel(c
         return x;
       };
       if (kWide) load_words(0);
+      if (kKeys) asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
       asm volatile("griddepcontrol.wait;" ::: "memory");
       const int2 both = book_exponents();
       const int e = kKeys ? both.x : both.y;
@@ -680,6 +702,8 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, 1) prefix_mma_kernel(c
         }
         asm volatile("bar.sync %0, %1;" ::"n"(kKeys ? 1 : 2), "n"(32 * kWarps) : "memory");
       }
+      Phase step;
+      if (kKeys && !kWide) step.get(steps);       // 64-scalar groups have no registers for it
       for (int i = 0; i < ntiles; ++i) {
         const int s = kStages == 2 ? i & 1 : 0, lap = i / kStages;
         auto stage_free = [&] { return lap == 0 || wait(empty + s, (lap - 1) & 1, a.fault); };
@@ -718,8 +742,9 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, 1) prefix_mma_kernel(c
             for (int u = 0; u < 2; ++u) {
               if (kKeys) {
                 store(s, u0 + u, ph.rotate(x[u]));
-                if (u0 + u < kPer - 1) ph.turn(step);
-                else ph.turn(jump);
+                Phase w;
+                w.get(u0 + u < kPer - 1 ? steps : jumps);
+                ph.turn(w);
               } else {
                 uint4 v = make_uint4(half_pair(x[u][0], x[u][1]), half_pair(x[u][2], x[u][3]), half_pair(x[u][4], x[u][5]),
                                      half_pair(x[u][6], x[u][7]));
@@ -731,16 +756,16 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, 1) prefix_mma_kernel(c
         } else {
           uint64_t* c_full = &ctl.c_full[kKeys ? 0 : 1][i % kCodeStages];
           if (!wait(c_full, (i / kCodeStages) & 1, a.fault)) break;
-          uint32_t w[kPer * R];
+          uint32_t codes_of[kPer * R];
 #pragma unroll
-          for (int j = 0; j < kPer * R; ++j) w[j] = code(i, j / R, j % R);
+          for (int j = 0; j < kPer * R; ++j) codes_of[j] = code(i, j / R, j % R);
           constexpr int kBatch = kPer < 4 ? kPer : 4;                        // gathers in flight
           bool ok = true;
 #pragma unroll
           for (int u0 = 0; u0 < kPer; u0 += kBatch) {
             uint4 v[kBatch * R];
 #pragma unroll
-            for (int j = 0; j < kBatch * R; ++j) v[j] = lds16(book + (j % R) * (kCodes * CH * 16) + w[u0 * R + j] * (CH * 16));
+            for (int j = 0; j < kBatch * R; ++j) v[j] = lds16(book + (j % R) * (kCodes * CH * 16) + codes_of[u0 * R + j] * (CH * 16));
             if (u0 == 0) ok = stage_free();
             if (!ok) break;
 #pragma unroll

@@ -187,16 +187,19 @@ size_t cvq_paged_workspace_bytes(const cvq_paged* p, int n_splits) {
 
 int cvq_paged_suggest_splits(const cvq_paged* p, int sm_count) {
   if (check_paged(p) != CVQ_OK || sm_count < 1) return 1;
-  // A split holds 256 tokens or more: on a window of 128 tokens one split takes 7.3 us where
+  // A split holds 256 tokens or more (512 where there are few splits): on a window of 128 tokens one split takes 7.3 us where
   // two, with their merge, take 14.  Beyond that a CTA per SM carries one sequence best (131071
   // tokens: 18 splits of 8 KV heads 88.9 us, 37 splits 94.8), and of several sequences, whose
   // lengths differ, two CTAs per SM (16 sequences of 1024 to 8192: 3 splits 54.1 us, 2 64.2).
   const long long tokens = static_cast<long long>(p->max_pages) * p->page_size;
   const long long units = static_cast<long long>(p->batch) * p->n_kv_heads;
-  const long long most = std::max(1LL, tokens / 256);
   const long long ctas = p->batch == 1 ? sm_count : 2LL * sm_count;
-  long long n = ctas / units;
-  if (p->batch > 1 && n < 4) n = (ctas + units - 1) / units;
+  long long n = ctas / units, least = 256;
+  if (p->batch > 1 && n < 4) {
+    n = (ctas + units - 1) / units;
+    least = 512;                                  // 16 sequences of 800: one split 14.1 us, three 19.9
+  }
+  const long long most = std::max(1LL, tokens / least);
   return static_cast<int>(std::max(1LL, std::min({4096LL, most, n})));
 }
 
