@@ -6,6 +6,10 @@
 // from shared memory as float4 along the 128 dims (token rows padded to 132 floats: the 8
 // lanes of a 16-byte phase then start 4 banks apart); the weights go through shared memory
 // transposed so that O += P V reads RPT weights and 8 value dims per thread and token.
+//
+// What bounds it: shared-memory operands (for 64 rows 8 float4 loads per 64 FMA, for up to 16 rows,
+// where a thread has one row, 5 per 16) and, for one tile per CTA, its chain of two gathers.  4
+// sequences over 1000 tokens, R = 1, 12.9 us with the merge; 16 over 8192 95 us.
 #include "serve.cuh"
 
 namespace cvq {

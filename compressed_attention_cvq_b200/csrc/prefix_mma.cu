@@ -13,24 +13,32 @@
 //                        ones to the others, each with its own O, maximum and sum (joined at
 //                        the end), so that the exponentials of one tile run under the other's
 //                        loads and barriers
-// What bounds it: exponentials (16 a clock and SM), matrix products and the producers' issue
-// slots are within 1.3 of one another for 128 rows; below that the producers.
+// What bounds it: for 128 rows no one unit (the exponentials, the products, the FMA pipe and the
+// gathers take a fifth to a third of their rates each, the issue slots half); for fewer rows the
+// producers.  Measured in a captured graph, 32 query and 8 KV heads: 32 sequences over 131072
+// tokens, R = 1, 105 us (660 TFLOP/s of 1646, the floor is 42 us); 16 over 32768, R = 2, 43 us, and
+// R = 11 of 64-scalar groups 117 us; a short prefix 12 us, of which the first tile's scores come
+// after 5 (the codebooks' conversion 3) and the join and merge take 4.
 //
 // Bank conflicts: codebooks lie as [round][code][chunk of 8 dims], so 8 lanes that work on the
 // 8 (or 16) chunks of one token read 8 different bank groups whatever their codes are.
 //
 // Codebooks that exceed one SM (two rounds of 8-scalar groups, 64-scalar groups) are split by
 // dims over a pair of CTAs: each decodes its 64 dims of both CTAs' tokens and stores the other
-// CTA's half through distributed shared memory.
+// CTA's half through distributed shared memory (st.async: 53 us where stores and a fence took 97).
 //
 // Phases: a producer thread keeps e^{i theta t} of its 4 pairs in fp32 and turns them on from
 // token to token; every 64 tiles they are taken anew from the exact turns, which holds their
 // error below 2^-15 (2^-19 typical), far under the operands' 2^-12.
 //
-// Roundings: codewords, the rotated sum and the weights are rounded to fp16 (2^-12 at most
-// each), sums of rounds and everything after the products stay in fp32, except that two value
-// codewords (8-scalar groups) are added as fp16: that sum would be rounded to fp16 next anyhow.
-// Codebooks are scaled by a power of two into fp16's range, and so is each query row.
+// Roundings to fp16, 2^-11 at most each: a codeword; the sum of two codewords of 8-scalar groups
+// and of neighbouring rounds of 64-scalar groups (the rounds' total is fp32 there); for 8-scalar
+// groups the sine and cosine and the two products of a rotation, whose fp16 arithmetic takes half
+// the instructions of fp32 and conversions (124 us -> 116); the rotated key; the value; the
+// weight.  A score is then off by 5e-4 of its terms' root mean square, a value by 3e-4, at random
+// from token to token: below bf16's own rounding of the output, and averaged over the softmax in
+// lse.  Codebooks and query rows are scaled by powers of two into fp16's range.  Products are
+// summed, and the softmax, O and the merge kept, in fp32.
 #include <type_traits>
 
 #include "serve.cuh"
