@@ -37,49 +37,46 @@ __device__ __forceinline__ void put8(float* at, const float (&x)[8]) {
   reinterpret_cast<float4*>(at)[1] = make_float4(x[4], x[5], x[6], x[7]);
 }
 
-// A tile of keys and values, decoded, the keys rotated by their positions.  A thread makes chunk
-// c = tid % 16 (8 dims) of kPer tokens, all of whose codes it loads before the first codeword and
-// all of whose codewords before the first sum (8-scalar groups, kR rounds; 64-scalar groups,
-// kR = 0, go round by round).  Tokens from `end` on are zeros.
+// One side of a tile: 8 dims (chunk c = tid % 16) of kPer tokens a thread, all of whose codes are
+// loaded before the first codeword and all of whose codewords before the first sum (8-scalar
+// groups, kR rounds; 64-scalar groups, kR = 0, go round by round).
+constexpr int kPer = kTile * 16 / kThreads, kStep = kThreads / 16;
 template <int kR>
-__device__ __forceinline__ void make_tile(const ServeArgs& a, const unsigned long long* f_tab, int h, int t0, int end,
-                                          float* sk, float* sv) {
-  constexpr int kPer = kTile * 16 / kThreads, kStep = kThreads / 16;
+__device__ __forceinline__ void decode_side(const ServeArgs& a, const float* cb, const uint8_t* codes, int h, int t0, int end,
+                                            float (&x)[kPer][8]) {
   const int c = threadIdx.x & 15, tk = threadIdx.x >> 4;
-  const float* kcb = a.key_cb + h * a.key_cb_stride;
-  const float* vcb = a.val_cb + h * a.val_cb_stride;
-  float k[kPer][8], v[kPer][8];
 #pragma unroll
   for (int u = 0; u < kPer; ++u)
 #pragma unroll
-    for (int d = 0; d < 8; ++d) k[u][d] = v[u][d] = 0.f;
+    for (int d = 0; d < 8; ++d) x[u][d] = 0.f;
   if constexpr (kR > 0) {
-    int kc[kPer * kR], vc[kPer * kR];
+    int code[kPer * kR];
 #pragma unroll
     for (int j = 0; j < kPer * kR; ++j) {
       const int t = min(t0 + tk + j / kR * kStep, end - 1);
-      const size_t row = ((static_cast<size_t>(h) * a.t_cap + t) * kR + j % kR) * kGroups + c;
-      kc[j] = __ldg(a.key_codes + row);
-      vc[j] = __ldg(a.val_codes + row);
+      code[j] = __ldg(codes + ((static_cast<size_t>(h) * a.t_cap + t) * kR + j % kR) * kGroups + c);
     }
 #pragma unroll
-    for (int j = 0; j < kPer * kR; ++j) {
-      const size_t base = (static_cast<size_t>(c) * kR + j % kR) * kCodes;
-      add8(k[j / kR], kcb + (base + kc[j]) * kCodeword);
-      add8(v[j / kR], vcb + (base + vc[j]) * kVDims);
-    }
+    for (int j = 0; j < kPer * kR; ++j) add8(x[j / kR], cb + ((static_cast<size_t>(c) * kR + j % kR) * kCodes + code[j]) * kCodeword);
   } else {
     const int G = c >> 3;
     for (int r = 0; r < a.R; ++r) {
-      const size_t base = (static_cast<size_t>(G) * a.R + r) * kWideCodes;
+      const float* book = cb + (static_cast<size_t>(G) * a.R + r) * (kWideCodes * kWideGroupDim) + 8 * (c & 7);
 #pragma unroll
-      for (int u = 0; u < kPer; ++u) {
-        const int t = min(t0 + tk + u * kStep, end - 1);
-        add8(k[u], kcb + (base + wide_code(a.key_codes, a, h, G, r, t)) * kWideGroupDim + 8 * (c & 7));
-        add8(v[u], vcb + (base + wide_code(a.val_codes, a, h, G, r, t)) * kWideGroupDim + 8 * (c & 7));
-      }
+      for (int u = 0; u < kPer; ++u)
+        add8(x[u], book + wide_code(codes, a, h, G, r, min(t0 + tk + u * kStep, end - 1)) * kWideGroupDim);
     }
   }
+}
+
+// A tile of keys and values, decoded, the keys rotated by their positions; tokens from `end` on
+// are zeros.
+template <int kR>
+__device__ __forceinline__ void make_tile(const ServeArgs& a, const unsigned long long* f_tab, int h, int t0, int end,
+                                          float* sk, float* sv) {
+  const int c = threadIdx.x & 15, tk = threadIdx.x >> 4;
+  float x[kPer][8];
+  decode_side<kR>(a, a.key_cb + h * a.key_cb_stride, a.key_codes, h, t0, end, x);
   // phases of the first token, turned on to the others (one fp32 rounding each)
   float2 ph[4], step[4];
 #pragma unroll
@@ -95,26 +92,34 @@ __device__ __forceinline__ void make_tile(const ServeArgs& a, const unsigned lon
       for (int p = 0; p < 4; ++p)
         ph[p] = make_float2(ph[p].x * step[p].x - ph[p].y * step[p].y, ph[p].x * step[p].y + ph[p].y * step[p].x);
     }
-    if (t0 + row < end) {
+    const bool in = t0 + row < end;
 #pragma unroll
-      for (int p = 0; p < 4; ++p) {
-        const float re = k[u][2 * p], im = k[u][2 * p + 1];
-        k[u][2 * p] = re * ph[p].x - im * ph[p].y;
-        k[u][2 * p + 1] = re * ph[p].y + im * ph[p].x;
-      }
-    } else {
-#pragma unroll
-      for (int d = 0; d < 8; ++d) k[u][d] = v[u][d] = 0.f;
+    for (int p = 0; p < 4; ++p) {
+      const float re = x[u][2 * p], im = x[u][2 * p + 1];
+      x[u][2 * p] = in ? re * ph[p].x - im * ph[p].y : 0.f;
+      x[u][2 * p + 1] = in ? re * ph[p].y + im * ph[p].x : 0.f;
     }
-    put8(sk + row * kPad + 8 * c, k[u]);
-    put8(sv + row * kHeadDim + 8 * c, v[u]);
+    put8(sk + row * kPad + 8 * c, x[u]);
+  }
+  decode_side<kR>(a, a.val_cb + h * a.val_cb_stride, a.val_codes, h, t0, end, x);
+#pragma unroll
+  for (int u = 0; u < kPer; ++u) {
+    const int row = tk + u * kStep;
+    if (t0 + row >= end) {
+#pragma unroll
+      for (int d = 0; d < 8; ++d) x[u][d] = 0.f;
+    }
+    put8(sv + row * kHeadDim + 8 * c, x[u]);
   }
 }
 
 // RB query rows per CTA: the rows of a KV head are (sequence, head of the group) pairs, and
 // blockIdx.z takes RB of them.
-template <int RB>
-__global__ void __launch_bounds__(kThreads, RB == 16 ? 2 : 1) attend_f32_kernel(const __grid_constant__ ServeArgs a) {
+// Two CTAs an SM where they have room for it, but one of 64 rows and 8-scalar groups: a second one's
+// tiles would take the L1 cache that its codewords are gathered through (R = 2: 110 us against 125;
+// 64-scalar groups 119 against 101).
+template <int RB, bool kWide>
+__global__ void __launch_bounds__(kThreads, RB == 16 || kWide ? 2 : 1) attend_f32_kernel(const __grid_constant__ ServeArgs a) {
   constexpr int RPT = RB / 16;
   extern __shared__ float4 smem4[];
   float* sq = reinterpret_cast<float*>(smem4);      // [RB][kPad]
@@ -185,7 +190,7 @@ __global__ void __launch_bounds__(kThreads, RB == 16 ? 2 : 1) attend_f32_kernel(
   }
   for (int t0 = start; t0 < end; t0 += kTile) {
     __syncthreads();                                // the last tile's readers are done
-    if (a.wide) make_tile<0>(a, f_tab, h, t0, end, sk, sv);
+    if constexpr (kWide) make_tile<0>(a, f_tab, h, t0, end, sk, sv);
     else if (a.R == 1) make_tile<1>(a, f_tab, h, t0, end, sk, sv);
     else make_tile<2>(a, f_tab, h, t0, end, sk, sv);
     if (RB == 16 && t0 == start) put_query(tid, early);
@@ -350,14 +355,14 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_kernel(const __grid_co
   if (lane == 0) a.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
 }
 
-template <int RB>
+template <int RB, bool kWide>
 cudaError_t run(const ServeArgs& a, dim3 grid, cudaStream_t stream) {
   static PerDeviceFlag flag;
   const size_t bytes = (static_cast<size_t>(RB) * kPad + kTile * kPad + kTile * kHeadDim) * sizeof(float);
   static_assert(RB <= kPad, "the weights fit over the keys");
-  const cudaError_t e = set_smem_limit_once(flag, attend_f32_kernel<RB>, bytes);
+  const cudaError_t e = set_smem_limit_once(flag, attend_f32_kernel<RB, kWide>, bytes);
   if (e != cudaSuccess) return e;
-  return launch_chained(attend_f32_kernel<RB>, grid, kThreads, a, stream, bytes);
+  return launch_chained(attend_f32_kernel<RB, kWide>, grid, kThreads, a, stream, bytes);
 }
 
 }  // namespace
@@ -365,7 +370,8 @@ cudaError_t run(const ServeArgs& a, dim3 grid, cudaStream_t stream) {
 cudaError_t launch_prefix_f32(const ServeArgs& a, cudaStream_t stream) {
   const int rows = a.batch * a.group;
   const dim3 grid(a.n_splits, a.n_kv_heads, rows <= 16 ? 1 : (rows + 63) / 64);
-  return rows <= 16 ? run<16>(a, grid, stream) : run<64>(a, grid, stream);
+  if (rows <= 16) return a.wide ? run<16, true>(a, grid, stream) : run<16, false>(a, grid, stream);
+  return a.wide ? run<64, true>(a, grid, stream) : run<64, false>(a, grid, stream);
 }
 
 cudaError_t launch_merge(const ServeArgs& a, cudaStream_t stream) {
