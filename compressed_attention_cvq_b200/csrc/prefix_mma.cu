@@ -78,16 +78,18 @@ struct Control {
 };
 
 // ---- PTX ----
-__device__ __forceinline__ bool wait(uint64_t* bar, unsigned parity, unsigned int* fault) {
-  const uint32_t addr = smem_u32(bar);
+__device__ __forceinline__ bool try_wait(uint32_t bar, unsigned parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+      : "=r"(done) : "r"(bar), "r"(parity) : "memory");
+  return done != 0;
+}
+// the bounded rest of a wait, out of line: the waits are in every role's loop
+__device__ __noinline__ bool wait_on(uint32_t bar, unsigned parity, unsigned int* fault) {
   unsigned long long t0 = 0;
   for (unsigned i = 1;; ++i) {
-    uint32_t done;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-        " selp.u32 %0, 1, 0, p;\n}"
-        : "=r"(done) : "r"(addr), "r"(parity) : "memory");
-    if (done) return true;
+    if (try_wait(bar, parity)) return true;
     if (i % 64 == 0) {                            // the clock is slow to read: now and then
       unsigned long long now;
       asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(now));
@@ -98,6 +100,13 @@ __device__ __forceinline__ bool wait(uint64_t* bar, unsigned parity, unsigned in
       }
     }
   }
+}
+__device__ __forceinline__ bool wait(uint64_t* bar, unsigned parity, unsigned int* fault) {
+  const uint32_t addr = smem_u32(bar);
+#pragma unroll 1
+  for (int i = 0; i < 64; ++i)
+    if (try_wait(addr, parity)) return true;
+  return wait_on(addr, parity, fault);
 }
 __device__ __forceinline__ void arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
