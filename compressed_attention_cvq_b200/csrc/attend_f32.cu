@@ -8,8 +8,8 @@
 // transposed so that O += P V reads RPT weights and 8 value dims per thread and token.
 //
 // What bounds it: shared-memory operands (for 64 rows 8 float4 loads per 64 FMA, for up to 16 rows,
-// where a thread has one row, 5 per 16) and, for one tile per CTA, its chain of two gathers.  4
-// sequences over 1000 tokens, R = 1, 12.9 us with the merge; 16 over 8192 95 us.
+// where a thread has two, 6 per 32) and, for one tile per CTA, its chain of two gathers.  4 sequences
+// over 1000 tokens, R = 1, 10.9 us with the merge; 16 over 8192 95 us.
 #include "serve.cuh"
 
 namespace cvq {
@@ -120,14 +120,18 @@ __device__ __forceinline__ void make_tile(const ServeArgs& a, const unsigned lon
 // 64-scalar groups 119 against 101).
 template <int RB, bool kWide>
 __global__ void __launch_bounds__(kThreads, RB == 16 || kWide ? 2 : 1) attend_f32_kernel(const __grid_constant__ ServeArgs a) {
-  constexpr int RPT = RB / 16;
+  // few rows: the threads are two halves, which share the dims of the scores and the tokens of the
+  // outputs, so that a thread has two rows and reads fewer operands per product
+  constexpr int kHalves = RB == 16 ? 2 : 1, RPT = RB * kHalves / 16;
   extern __shared__ float4 smem4[];
   float* sq = reinterpret_cast<float*>(smem4);      // [RB][kPad]
   float* sk = sq + RB * kPad;                       // [kTile][kPad]
   float* sv = sk + kTile * kPad;                    // [kTile][128]
   float* sp = sk;                                   // [kTile][RB], over the keys once they are read
+  float* sum = sk + kTile * RB;                     // [2][RB][kTile], two halves' scores, also over the keys
+  static_assert(kHalves == 1 || kTile * RB + 2 * RB * kTile <= kTile * kPad, "they fit");
   __shared__ unsigned long long f_tab[kPairs];
-  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  const int tid = threadIdx.x, tx = tid & 15, half = kHalves == 2 ? tid >> 7 : 0, ty = (tid >> 4) & (16 / kHalves - 1);
   asm volatile("griddepcontrol.wait;" ::: "memory");                        // for what ran before this call
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");         // the merge
   const int split = blockIdx.x, h = blockIdx.y;
@@ -201,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, RB == 16 || kWide ? 2 : 1) attend_f3
 #pragma unroll
       for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
 #pragma unroll 4
-    for (int d = 0; d < kHeadDim; d += 4) {
+    for (int d = half * (kHeadDim / kHalves); d < (half + 1) * (kHeadDim / kHalves); d += 4) {
       float4 qv[RPT], kv[4];
 #pragma unroll
       for (int i = 0; i < RPT; ++i) qv[i] = *reinterpret_cast<const float4*>(sq + (ty * RPT + i) * kPad + d);
@@ -218,6 +222,18 @@ __global__ void __launch_bounds__(kThreads, RB == 16 || kWide ? 2 : 1) attend_f3
         }
     }
     __syncthreads();                                // sp takes the place of sk
+    if constexpr (kHalves == 2) {
+      auto at = [&](int w, int i, int j) -> float& { return sum[(w * RB + ty * RPT + i) * kTile + tx + 16 * j]; };
+#pragma unroll
+      for (int i = 0; i < RPT; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) at(half, i, j) = s[i][j];
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < RPT; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[i][j] += at(1 - half, i, j);
+    }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       if (t0 + tx + 16 * j >= end) {
@@ -234,27 +250,28 @@ __global__ void __launch_bounds__(kThreads, RB == 16 || kWide ? 2 : 1) attend_f3
       const float ref = mn == -INFINITY ? 0.f : mn;          // nothing seen yet: every weight 0
       const float alpha = exp2f(m[i] - ref);
       m[i] = mn;
-      float sum = 0.f;
+      float total = 0.f;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const float p = exp2f(s[i][j] - ref);
-        sum += p;
-        sp[(tx + 16 * j) * RB + ty * RPT + i] = p;
+        total += p;
+        if (half == 0) sp[(tx + 16 * j) * RB + ty * RPT + i] = p;
       }
-      l[i] = fmaf(l[i], alpha, sum);
+      l[i] = fmaf(l[i], alpha, total);
 #pragma unroll
       for (int d = 0; d < 8; ++d) o[i][d] *= alpha;
     }
     __syncthreads();
 #pragma unroll 8
-    for (int t = 0; t < kTile; ++t) {
+    for (int t = half * (kTile / kHalves); t < (half + 1) * (kTile / kHalves); ++t) {
       float p[RPT];
       if constexpr (RPT == 4) {
         const float4 pv = *reinterpret_cast<const float4*>(sp + t * RB + ty * RPT);
         p[0] = pv.x; p[1] = pv.y; p[2] = pv.z; p[3] = pv.w;
       } else {
-#pragma unroll
-        for (int i = 0; i < RPT; ++i) p[i] = sp[t * RB + ty * RPT + i];
+        static_assert(RPT == 2 || RPT == 4, "rows of a thread");
+        const float2 pv = *reinterpret_cast<const float2*>(sp + t * RB + ty * RPT);
+        p[0] = pv.x; p[1] = pv.y;
       }
       const float4 v0 = *reinterpret_cast<const float4*>(sv + t * kHeadDim + 4 * tx);
       const float4 v1 = *reinterpret_cast<const float4*>(sv + t * kHeadDim + 64 + 4 * tx);
@@ -269,6 +286,25 @@ __global__ void __launch_bounds__(kThreads, RB == 16 || kWide ? 2 : 1) attend_f3
         o[i][6] = fmaf(p[i], v1.z, o[i][6]);
         o[i][7] = fmaf(p[i], v1.w, o[i][7]);
       }
+    }
+  }
+  if constexpr (kHalves == 2) {
+    __syncthreads();                                // the weights have been read
+    float4* other = reinterpret_cast<float4*>(sk) + (ty * RPT) * (kHeadDim / 4) + tx;
+    if (half == 1) {
+#pragma unroll
+      for (int i = 0; i < RPT; ++i) {
+        other[i * (kHeadDim / 4)] = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
+        other[i * (kHeadDim / 4) + 16] = make_float4(o[i][4], o[i][5], o[i][6], o[i][7]);
+      }
+    }
+    __syncthreads();
+    if (half == 1) return;
+#pragma unroll
+    for (int i = 0; i < RPT; ++i) {
+      const float4 u = other[i * (kHeadDim / 4)], v = other[i * (kHeadDim / 4) + 16];
+      o[i][0] += u.x; o[i][1] += u.y; o[i][2] += u.z; o[i][3] += u.w;
+      o[i][4] += v.x; o[i][5] += v.y; o[i][6] += v.z; o[i][7] += v.w;
     }
   }
 #pragma unroll
