@@ -2,11 +2,13 @@
 //
 // One pass: every element is read once and written once, so memory bounds it (a long prompt)
 // or the launch (a decode step).  A CTA takes a token, or some of its head rows where there are
-// few tokens.  All its threads first load their rows' chunks (16 threads a row, 8 dims each, up
-// to kRows rows a thread); under these loads two warps find the token's sequence and row and take
-// the sine and cosine of a pair a lane; one barrier, and the rows are rotated and stored.  (A warp
-// a token without a barrier measured 63 us on the 8192-token prompt, and every thread taking its
-// own sines 51 us; this 46, 4.3 TB/s.)  A decode step of 32 tokens takes 2.6 us.
+// few tokens.  All its threads first load their chunk of a row (16 bytes: 8 dims of 16-bit input, 4 of
+// fp32); under these loads two warps find the token's sequence and row and take
+// the sine and cosine of a pair a lane; one barrier, and the rows are rotated and stored.  Many
+// small CTAs with one chunk a thread in flight measured best: 8192 tokens of 32 + 16 heads in bf16 take
+// 42 us (4.8 TB/s; a copy of the same bytes by the framework 67), with 256 threads 45, with three
+// chunks a thread 56, a warp a token without a barrier 63; 1531 tokens of fp32 8.6 us (7.0 TB/s, some
+// of it from L2), a decode step of 32 tokens 2.5 us.
 #include <algorithm>
 
 #include "serve.cuh"
@@ -15,9 +17,7 @@ namespace cvq {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kSlots = kThreads / 16;       // rows that a CTA takes at once
-constexpr int kRows = 1;                    // rows in flight per thread: more CTAs instead measured best
+constexpr int kThreads = 128;
 
 template <typename T>
 __device__ __forceinline__ float to_float(T x);
@@ -36,34 +36,35 @@ __device__ __forceinline__ __nv_bfloat16 from_float(float x) { return __float2bf
 template <>
 __device__ __forceinline__ __half from_float(float x) { return __float2half_rn(x); }
 
-template <typename T>
-struct alignas(16) Chunk {
-  T x[8];
+template <typename T, int N>
+struct alignas(N * sizeof(T)) Chunk {
+  T x[N];
 };
 
+template <typename In>
+constexpr int kDims = 16 / sizeof(In);
+
 template <typename In, typename Kv>
-__global__ void __launch_bounds__(kThreads, 6) paged_append_kernel(const __grid_constant__ AppendArgs a) {
+__global__ void __launch_bounds__(kThreads, 12) paged_append_kernel(const __grid_constant__ AppendArgs a) {
+  constexpr int kD = kDims<In>, kLanes = kHeadDim / kD, kSlots = kThreads / kLanes;   // kSlots rows at once
   __shared__ float4 s_ph[kPairs / 2];                      // (cos, sin) of two pairs each
   __shared__ long long s_at;                               // element offset of the token's row of head 0; -1: none
   __shared__ bool s_live;
-  const int i = blockIdx.x, c = threadIdx.x & 15, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int i = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = threadIdx.x % kLanes;
   const int nq = a.q != nullptr ? a.n_q_heads : 0, nk = nq + a.n_kv_heads, heads = nk + a.n_kv_heads;   // queries, keys, values
   const int stride = gridDim.y * kSlots;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  Chunk<In> in[kRows];
-  auto load = [&](int r0) {
-#pragma unroll
-    for (int u = 0; u < kRows; ++u) {
-      const int r = r0 + u * stride;
-      if (r >= heads) continue;
+  Chunk<In, kD> in;
+  auto load = [&](int r) {
+    if (r < heads) {
       const In* src = r < nq ? static_cast<const In*>(a.q) + i * a.q_stride + r * kHeadDim
                     : r < nk ? static_cast<const In*>(a.k) + i * a.k_stride + (r - nq) * kHeadDim
                              : static_cast<const In*>(a.v) + i * a.v_stride + (r - nk) * kHeadDim;
-      in[u] = *reinterpret_cast<const Chunk<In>*>(src + 8 * c);
+      in = *reinterpret_cast<const Chunk<In, kD>*>(src + kD * c);
     }
   };
-  int r0 = blockIdx.y * kSlots + (threadIdx.x >> 4);
-  load(r0);
+  int r = blockIdx.y * kSlots + threadIdx.x / kLanes;
+  load(r);
   if (warp < kPairs / 32) {
     // the sequence: as many as end at or before i (offsets do not decrease); 32 probes at a time
     int b = 0, n = a.batch;
@@ -101,49 +102,47 @@ __global__ void __launch_bounds__(kThreads, 6) paged_append_kernel(const __grid_
   __syncthreads();
   if (!s_live) return;
   const long long at = s_at;
-  const float4 p0 = s_ph[2 * c], p1 = s_ph[2 * c + 1];
-  const float co[4] = {p0.x, p0.z, p1.x, p1.z}, si[4] = {p0.y, p0.w, p1.y, p1.w};
-  while (r0 < heads) {
+  float4 ph[kD / 4];                                       // (cos, sin) of two pairs each
 #pragma unroll
-    for (int u = 0; u < kRows; ++u) {
-      const int r = r0 + u * stride;
-      if (r >= heads) continue;
-      float x[8];
+  for (int v = 0; v < kD / 4; ++v) ph[v] = s_ph[c * (kD / 4) + v];
+  while (r < heads) {
+    float x[kD];
 #pragma unroll
-      for (int d = 0; d < 8; ++d) x[d] = to_float(in[u].x[d]);
-      if (r < nk) {
+    for (int d = 0; d < kD; ++d) x[d] = to_float(in.x[d]);
+    if (r < nk) {
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const float re = x[2 * v], im = x[2 * v + 1];
-          x[2 * v] = re * co[v] - im * si[v];
-          x[2 * v + 1] = re * si[v] + im * co[v];
-        }
-      }
-      if (r < nq) {
-        Chunk<In> out;
-#pragma unroll
-        for (int d = 0; d < 8; ++d) out.x[d] = from_float<In>(x[d]);
-        *reinterpret_cast<Chunk<In>*>(static_cast<In*>(a.q_out) + (static_cast<size_t>(i) * nq + r) * kHeadDim + 8 * c) = out;
-      } else if (at >= 0) {
-        Kv* pool = static_cast<Kv*>(r < nk ? a.k_pages : a.v_pages);
-        const int h = r < nk ? r - nq : r - nk;
-        Chunk<Kv> out;
-#pragma unroll
-        for (int d = 0; d < 8; ++d) out.x[d] = from_float<Kv>(x[d]);
-        *reinterpret_cast<Chunk<Kv>*>(pool + at + (static_cast<long long>(h) << a.page_shift) * kHeadDim + 8 * c) = out;
+      for (int v = 0; v < kD / 2; ++v) {
+        const float re = x[2 * v], im = x[2 * v + 1];
+        const float co = v % 2 == 0 ? ph[v / 2].x : ph[v / 2].z, si = v % 2 == 0 ? ph[v / 2].y : ph[v / 2].w;
+        x[2 * v] = re * co - im * si;
+        x[2 * v + 1] = re * si + im * co;
       }
     }
-    r0 += kRows * stride;
-    load(r0);
+    if (r < nq) {
+      Chunk<In, kD> out;
+#pragma unroll
+      for (int d = 0; d < kD; ++d) out.x[d] = from_float<In>(x[d]);
+      *reinterpret_cast<Chunk<In, kD>*>(static_cast<In*>(a.q_out) + (static_cast<size_t>(i) * nq + r) * kHeadDim + kD * c) = out;
+    } else if (at >= 0) {
+      Kv* pool = static_cast<Kv*>(r < nk ? a.k_pages : a.v_pages);
+      const int h = r < nk ? r - nq : r - nk;
+      Chunk<Kv, kD> out;
+#pragma unroll
+      for (int d = 0; d < kD; ++d) out.x[d] = from_float<Kv>(x[d]);
+      *reinterpret_cast<Chunk<Kv, kD>*>(pool + at + (static_cast<long long>(h) << a.page_shift) * kHeadDim + kD * c) = out;
+    }
+    r += stride;
+    load(r);
   }
 }
 
 template <typename In>
 cudaError_t launch_in(const AppendArgs& a, int kv_dtype, cudaStream_t stream) {
   const int heads = (a.q != nullptr ? a.n_q_heads : 0) + 2 * a.n_kv_heads;
-  // where there are fewer tokens than make 8 CTAs an SM of 148, several CTAs share a token's rows
+  // where there are fewer tokens than make 12 CTAs an SM of 148, several CTAs share a token's rows
+  constexpr int kSlots = kThreads / (kHeadDim / kDims<In>);
   const int most = (heads + kSlots - 1) / kSlots;
-  const dim3 grid(a.n_tokens, std::max(1, std::min(most, 8 * 148 / a.n_tokens)));
+  const dim3 grid(a.n_tokens, std::max(1, std::min(most, 12 * 148 / a.n_tokens)));
   return kv_dtype == CVQ_BF16 ? launch_chained(paged_append_kernel<In, __nv_bfloat16>, grid, kThreads, a, stream)
                               : launch_chained(paged_append_kernel<In, __half>, grid, kThreads, a, stream);
 }
