@@ -17,7 +17,7 @@
 // gathers take a fifth to a third of their rates each, the issue slots half); for fewer rows the
 // producers.  Measured in a captured graph, 32 query and 8 KV heads: 32 sequences over 131072
 // tokens, R = 1, 105 us (660 TFLOP/s of 1646, the floor is 42 us); 16 over 32768, R = 2, 43 us, and
-// R = 11 of 64-scalar groups 117 us; a short prefix 12 us, of which the first tile's scores come
+// R = 11 of 64-scalar groups 111 us; a short prefix 12 us, of which the first tile's scores come
 // after 5 (the codebooks' conversion 3) and the join and merge take 4.
 //
 // Bank conflicts: codebooks lie as [round][code][chunk of 8 dims], so 8 lanes that work on the
@@ -26,6 +26,8 @@
 // Codebooks that exceed one SM (two rounds of 8-scalar groups, 64-scalar groups) are split by
 // dims over a pair of CTAs: each decodes its 64 dims of both CTAs' tokens and stores the other
 // CTA's half through distributed shared memory (st.async: 53 us where stores and a fence took 97).
+// Of more than 11 rounds of 64-scalar groups the others are gathered from the workspace's copy of
+// the codebooks, from L2 (16 sequences over 4096 tokens, R = 21: 56 us; in fp32 151).
 //
 // Phases: a producer thread keeps e^{i theta t} of its 4 pairs in fp32 and turns them on from
 // token to token; every 64 tiles they are taken anew from the exact turns, which holds their
@@ -319,6 +321,10 @@ __host__ __device__ constexpr int book_items(int R) {
 }
 // Keys are held, here and in the operand tiles, with the two real and the two imaginary parts of
 // two pairs side by side, so that a pair of fp16 numbers rotates in one instruction each.
+template <bool kWide>
+__host__ __device__ constexpr int held_rounds(int R) {
+  return kWide && R > kWideRoundsPerCta ? kWideRoundsPerCta : R;
+}
 __device__ __forceinline__ uint4 scaled_halves(float4 x, float4 y, float scale, bool keys) {
   if (keys) {
     const float4 a = x, b = y;
@@ -392,7 +398,10 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, 1) prefix_mma_kernel(c
   const uint32_t tiles_k = smem_u32(smem), tiles_v = tiles_k + 2 * kTile;
   const uint32_t cb_k = tiles_v + kVStages * kTile;
   const int rounds = kWide ? a.R : R;
-  const uint32_t cb_bytes = kWide ? rounds * kWideCodes * 128 : R * kCodes * CH * 16;
+  // rounds of a codebook in shared memory; more are gathered from the workspace's copy, from L2
+  constexpr int kHeldRounds = held_rounds<kWide>(R);
+  const int held = min(rounds, kHeldRounds);
+  const uint32_t cb_bytes = kWide ? held * kWideCodes * 128 : R * kCodes * CH * 16;
   const uint32_t cb_v = cb_k + cb_bytes;
   // a stage of codes: keys, then values, [token][round][16 groups] as in the cache
   constexpr uint32_t kCodeBytes = kWide ? 0 : kGroupTok * R * kGroups;
@@ -673,11 +682,11 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, 1) prefix_mma_kernel(c
         anchor(0);
       }
       // 64-scalar groups: a word holds the codes of this slot's 4 tokens for a round; the 8 threads
-      // of a slot load two rounds each, a step ahead, and pass them around.  Packed codes: the word
+      // of a slot load two or three rounds each, a step ahead, and pass them around.  Packed codes: the word
       // is 24 bits from byte t / 4 * 3 of a row, in one or two aligned words; every row and step
       // has the same alignment (t_cap and steps are multiples of 64 tokens)
-      static_assert(!kWide || R <= 16, "two rounds a thread");
-      uint32_t lo[2], hi[2];
+      constexpr int kWords = kWide ? (R + 7) / 8 : 1;
+      uint32_t lo[kWords], hi[kWords];
       const unsigned shift = kWide && a.code_bits == 6 ? (3u * slot & 3u) * 8u : 0u;
       auto load_words = [&](int i) {
         const long long t = start + static_cast<long long>(i) * kGroupTok + 4 * slot;
@@ -685,7 +694,7 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, 1) prefix_mma_kernel(c
         const uint8_t* p = codes + ((static_cast<size_t>(h) * kWideGroups + rank) * rounds + cl) * row_bytes +
                            (a.code_bits == 6 ? t / 4 * 3 - (shift >> 3) : t);
 #pragma unroll
-        for (int k = 0; k < 2; ++k, p += 8 * row_bytes) {
+        for (int k = 0; k < kWords; ++k, p += 8 * row_bytes) {
           lo[k] = hi[k] = 0u;
           if (cl + 8 * k < rounds && t < end) {
             lo[k] = __ldg(reinterpret_cast<const uint32_t*>(p));
@@ -713,7 +722,7 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, 1) prefix_mma_kernel(c
       if (e != kUsualScale) {                     // far from the usual size: scaled anew, from the codebook itself
         const float* cb = kKeys ? a.key_cb + static_cast<long long>(h) * a.key_cb_stride
                                 : a.val_cb + static_cast<long long>(h) * a.val_cb_stride;
-        for (int i = tid; i < book_items<C, kWide>(rounds); i += 32 * kWarps) {
+        for (int i = tid; i < book_items<C, kWide>(held); i += 32 * kWarps) {
           const float4* x = reinterpret_cast<const float4*>(book_item<C, kWide>(cb, rounds, rank, i));
           sts16((kKeys ? cb_k : cb_v) + i * 16, scaled_halves(__ldg(x), __ldg(x + 1), pow2(e), kKeys));
         }
@@ -721,19 +730,36 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, 1) prefix_mma_kernel(c
       }
       Phase step;
       if (kKeys && !kWide) step.get(steps);       // 64-scalar groups have no registers for it
+      // rounds beyond the held ones: this thread's 16 bytes of every codeword, in fp16 and in fp32
+      const unsigned char* far_book = static_cast<const unsigned char*>(a.book) +
+                                      ((static_cast<size_t>(h) * C + rank) * 2 + (kKeys ? 0 : 1)) * (static_cast<size_t>(rounds) * kWideCodes * 128) + cl * 16;
+      const float* far_cb = (kKeys ? a.key_cb + static_cast<long long>(h) * a.key_cb_stride : a.val_cb + static_cast<long long>(h) * a.val_cb_stride) +
+                            static_cast<size_t>(rank) * rounds * kWideCodes * 64 + cl * 8;
       for (int i = 0; i < ntiles; ++i) {
         const int s = kStages == 2 ? i & 1 : 0, lap = i / kStages;
         auto stage_free = [&] { return lap == 0 || wait(empty + s, (lap - 1) & 1, a.fault); };
         const long long left = end - (start + static_cast<long long>(i) * kGroupTok);
         if (kKeys && i % kReanchor == 0 && i > 0) anchor(i);
         if constexpr (kWide) {
-          uint32_t w[R];
-          {
-            const uint32_t w0 = __funnelshift_r(lo[0], hi[0], shift), w1 = __funnelshift_r(lo[1], hi[1], shift);
+          uint32_t own[kWords];
 #pragma unroll
-            for (int r = 0; r < R; ++r) w[r] = __shfl_sync(0xffffffffu, r < 8 ? w0 : w1, (lane & 24) | (r & 7));
-          }
-          if (i + 1 < ntiles) load_words(i + 1);
+          for (int k = 0; k < kWords; ++k) own[k] = __funnelshift_r(lo[k], hi[k], shift);
+          // every round's word now where the registers allow it, else when it is used
+          auto pass = [&](int r) { return __shfl_sync(0xffffffffu, own[r / 8], (lane & 24) | (r & 7)); };
+          constexpr bool kNow = R <= kWideRoundsPerCta;
+          uint32_t all[kNow ? R : 1];
+#pragma unroll
+          for (int r = 0; r < (kNow ? R : 0); ++r) all[r] = pass(r);
+          auto word = [&](int r) { return kNow ? all[kNow ? r : 0] : pass(r); };
+          auto codeword = [&](int r, uint32_t w, int u) {
+            const uint32_t at = entry(w, u);
+            if (r < kHeldRounds) return lds16(book + r * (kWideCodes * 128) + at);
+            if (e == kUsualScale)
+              return __ldg(reinterpret_cast<const uint4*>(far_book + r * (kWideCodes * 128) + at));
+            const float4* x = reinterpret_cast<const float4*>(far_cb + (r * (kWideCodes * 128) + at) / 2);
+            return scaled_halves(__ldg(x), __ldg(x + 1), pow2(e), kKeys);
+          };
+          if (i + 1 < ntiles) load_words(i + 1);      // own[] is taken
           if (!stage_free()) break;
 #pragma unroll
           for (int u0 = 0; u0 < kPer; u0 += 2) {
@@ -747,11 +773,13 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, 1) prefix_mma_kernel(c
 #pragma unroll
             for (int r = 0; r < R; r += 2) {
               if (r >= rounds) continue;
-              const bool both = r + 1 < R && r + 1 < rounds;
+              const int r1 = r + 1 < R ? r + 1 : r;
+              const bool both = r1 > r && r1 < rounds;
+              const uint32_t w0 = word(r), w1 = word(r1);
 #pragma unroll
               for (int u = 0; u < 2; ++u) {
-                uint4 y = lds16(book + r * (kWideCodes * 128) + entry(w[r], u0 + u));
-                if (both) y = add_chunks(y, lds16(book + (r + 1) * (kWideCodes * 128) + entry(w[r + 1 < R ? r + 1 : 0], u0 + u)));
+                uint4 y = codeword(r, w0, u0 + u);
+                if (both) y = add_chunks(y, codeword(r1, w1, u0 + u));
                 add_chunk(x[u], y);
               }
             }
@@ -830,9 +858,11 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, 1) prefix_mma_kernel(c
       asm volatile("griddepcontrol.wait;" ::: "memory");
       constexpr uint32_t kPiece = 16384;
       mbar_expect_tx(&ctl.book, 2 * cb_bytes);
-      const unsigned char* book = static_cast<const unsigned char*>(a.book) + (static_cast<size_t>(h) * C + rank) * (2 * cb_bytes);
-      for (uint32_t at = 0; at < 2 * cb_bytes; at += kPiece)
-        bulk_load(smem + (cb_k - tiles_k) + at, book + at, min(kPiece, 2 * cb_bytes - at), &ctl.book);
+      const uint32_t stored = kWide ? rounds * kWideCodes * 128 : cb_bytes;   // of keys or values in the workspace
+      const unsigned char* book = static_cast<const unsigned char*>(a.book) + (static_cast<size_t>(h) * C + rank) * (2 * static_cast<size_t>(stored));
+      for (uint32_t side = 0; side < 2; ++side)
+        for (uint32_t at = 0; at < cb_bytes; at += kPiece)
+          bulk_load(smem + (cb_k - tiles_k) + side * cb_bytes + at, book + side * stored + at, min(kPiece, cb_bytes - at), &ctl.book);
       if (!kWide) {
         bool ok = true;
         for (int i = first; ok && i < ntiles + 2; ++i) {                   // values are two steps behind
@@ -956,13 +986,13 @@ cudaError_t run(const ServeArgs& a, cudaStream_t stream) {
   static PerDeviceFlag flag;
   constexpr int kTiles = (kWide ? 3 : 4) * kTile;
   constexpr size_t kCodes8 = kWide ? 0 : kMostCodeStages / C * 2 * C * kTok * R * kGroups;
-  constexpr size_t kMost = kTiles + 32 * book_items<C, kWide>(R) + kCodes8 + sizeof(Control);
+  constexpr size_t kMost = kTiles + 32 * book_items<C, kWide>(held_rounds<kWide>(R)) + kCodes8 + sizeof(Control);
   static_assert(kMost <= 227 * 1024, "fits an SM");
   cudaError_t e = set_smem_limit_once(flag, prefix_mma_kernel<C, kWide, R>, kMost);
   if (e != cudaSuccess) return e;
   e = launch_chained(prefix_book_kernel<C, kWide>, dim3(book_items<C, kWide>(a.R) / kBookThreads, 2 * C, a.n_kv_heads), kBookThreads, a, stream);
   if (e != cudaSuccess) return e;
-  size_t bytes = kTiles + 32 * static_cast<size_t>(book_items<C, kWide>(a.R)) + kCodes8;
+  size_t bytes = kTiles + 32 * static_cast<size_t>(book_items<C, kWide>(held_rounds<kWide>(a.R))) + kCodes8;
   if (bytes < kOutBytes) bytes = kOutBytes;
   bytes += sizeof(Control);
   cudaLaunchAttribute attr[2];
@@ -985,7 +1015,7 @@ cudaError_t run(const ServeArgs& a, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_prefix_mma(const ServeArgs& a, cudaStream_t stream) {
-  if (a.wide) return run<2, true, kWideRoundsPerCta>(a, stream);
+  if (a.wide) return a.R <= kWideRoundsPerCta ? run<2, true, kWideRoundsPerCta>(a, stream) : run<2, true, kWideMaxR>(a, stream);
   return a.R == 1 ? run<1, false, 1>(a, stream) : run<2, false, 2>(a, stream);
 }
 

@@ -32,12 +32,11 @@ size_t round16(size_t n) { return (n + 15) / 16 * 16; }
 // CTAs of the tensor-core kernel that share a split (each leaves a partial state)
 int prefix_pair(const cvq_shape* s) { return !is_wide(s) && s->R == 1 ? 1 : 2; }
 
-// Whether the tensor-core kernel takes the call: 16-bit queries, rounds whose codebooks fit a pair
-// of SMs, and room for 512 tokens.  Its scores are off by 2^-11 each, which averages out over a
+// Whether the tensor-core kernel takes the call: 16-bit queries and room for 512 tokens.  Its scores are off by 2^-11 each, which averages out over a
 // softmax (lse of 512 tokens: 5e-6 relative) but not over a few tokens (64: 2e-5); and a prefix
 // that short takes either kernel the same time, that of the launches.
 bool prefix_on_tensor_cores(const cvq_shape* s, int q_dtype) {
-  return q_dtype != CVQ_F32 && (!is_wide(s) || s->R <= kWideRoundsPerCta) && s->t_cap >= 512;
+  return q_dtype != CVQ_F32 && s->t_cap >= 512;
 }
 
 // partial states of (sequence, query head) rows, 16-byte aligned

@@ -340,3 +340,25 @@ def test_long_streams_keep_their_phases():
     for R, group in ((1, 8), (2, 8), (2, 64)):
         d, dev = make(2, 4, 1, 30016, R, "fp16", group, seed=R)
         verify(d, call(cvq, dev, 30001, group, n_splits=1), 30001, "fp16")
+
+
+@pytest.mark.parametrize("R", [12, 13, 16, 17, 21])
+@pytest.mark.parametrize("scale", [1.0, 2.0 ** 25])
+def test_rounds_beyond_the_held_ones(R, scale):
+    """More rounds than a pair of SMs holds: the others come from the workspace's copy, or, where
+    their scale is not the usual one, from the codebooks."""
+    import compressed_attention_cvq_b200 as cvq
+    d, dev = make(7, 8, 2, 1024, R, "fp16", 64, seed=R)
+    for name in ("key_cb", "val_cb"):
+        d[name] = (d[name] * np.float32(scale)).astype(np.float32)
+        dev[name] = torch.from_numpy(d[name]).cuda()
+    if scale > 1:
+        # keys of 2^10 and queries of 2^-10, all exact, so that scores stay as they were
+        d["key_cb"] /= np.float32(scale / 2.0 ** 10)
+        dev["key_cb"] = torch.from_numpy(d["key_cb"]).cuda()
+        dev["q"] = (dev["q"].double() / 2.0 ** 10).half()
+    d["q"] = dev["q"].double().cpu().numpy()
+    got = call(cvq, dev, 1000, 64, 0, 2, out_dtype=torch.float32)
+    d["val_cb"] = d["val_cb"] / scale
+    verify(d, (got[0].double() / scale, got[1]), 1000, "fp16", "fp32")
+    assert cvq.fault_status(clear=True) == 0
