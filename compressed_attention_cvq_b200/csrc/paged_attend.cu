@@ -13,7 +13,9 @@
 // weights keep 16 bits (bf16 pages) or 22 bits (fp16 pages) at no extra instruction, since a
 // group has at most 8 heads.  For fp16 pages a query row is first scaled by a power of two
 // into fp16's range, and the weights are taken relative to 2^15 below the maximum, so that the
-// small ones stay normal numbers.  Scores, weights' sums and outputs accumulate in fp32.
+// small ones stay normal numbers.  bf16 has fp32's range: there they are taken relative to 2^-8, so
+// that sums of the largest values have room (the weights' sum, relative to the maximum, may reach
+// 2^136 over the largest value).  Scores, weights' sums and outputs accumulate in fp32.
 //
 // Measured in a captured graph, 8 KV heads, bf16 pages: 64 sequences of up to 16384 tokens 486 us
 // (6.6 TB/s, the rate of a copy), one of 131071 (fp16) 89 us (6.0 TB/s), 16 of 1024 to 8192 54 us
@@ -25,6 +27,8 @@
 // maximum, sum and output; the four are joined through shared memory at the end.  A CTA whose
 // split starts behind its sequence leaves at once, and the CTA of a (sequence, KV head) that
 // finishes last merges the splits (as in cvq_attend; the order of the sum is fixed).
+#include <type_traits>
+
 #include "serve.cuh"
 
 namespace cvq {
@@ -222,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attend_kernel(cons
 
   // ---- one pass over this warp's chunks ----
   // weights are 2^(s - ref), ref = running maximum - kLift
-  constexpr float kLift = 15.f;
+  constexpr float kLift = std::is_same<T, __half>::value ? 15.f : -8.f;
   float m = -INFINITY, l = 0.f;
   float o[16][4];
 #pragma unroll

@@ -488,3 +488,47 @@ def test_captured_behind_a_copy_a_memset_and_a_join(call):
         torch.cuda.synchronize()
         n = slice(None) if call != "append" else slice(0, 43)
         assert torch.equal(got[n], want[n]) and torch.equal(after[n], want[n])
+
+
+@pytest.mark.parametrize("cache,scale", [("bf16", 2.0 ** 125), ("fp16", 2.0 ** 13), ("bf16", 2.0 ** -120)])
+def test_values_near_the_ends_of_their_type(cache, scale):
+    """Sums of weights and values stay inside fp32 wherever the output does."""
+    import compressed_attention_cvq_b200 as cvq
+    a = list(setup([700, 64], 8, 2, 16, "bf16", cache, seed=14))
+    a[3] = (a[3].float().clamp(-1.9, 1.9) * scale).to(DT[cache])
+    for n in (1, 2):
+        out, lse = cvq.paged_attend(*a, n, out_dtype=torch.float32)
+        # in units of the scale, where the absolute terms of the tolerance belong
+        b = list(a)
+        b[3] = a[3].double() / scale
+        verify((out.double() / scale, lse), *b[1:], "bf16", cache, None, "fp32")
+
+
+def test_the_stream_argument():
+    import compressed_attention_cvq_b200 as cvq
+    st = torch.cuda.Stream()
+    a = setup([300, 50], 8, 2, 16, "bf16", "bf16", seed=3)
+    want = cvq.paged_attend(*a)
+    pg, q, k, v, off, lens, table, kp, vp = append_case([3, 40], [5, 0], 8, 2, 16, "bf16", "bf16", 1)
+    want_q = cvq.paged_append(pg, k, v, off, lens, table, kp, vp, q=q)
+    d = workloads.small(batch=1, n_q_heads=8, n_kv_heads=2, t_cap=640, R=2, seed=4)
+    dev = {n: torch.from_numpy(d[n]).cuda() for n in ("key_cb", "val_cb", "key_codes", "val_codes")}
+    x = torch.randn(4, 8, 128, device="cuda").bfloat16()
+    shape, ln = cvq.shape_of(x, dev["key_codes"]), i32([600])
+
+    def prefix(**kw):
+        return cvq.prefix_attend(shape, x, dev["key_cb"], dev["key_codes"], dev["val_codes"], ln,
+                                 dev["val_cb"], **kw)
+    want_p = prefix()
+    outs = [[torch.zeros_like(y) for y in w] for w in (want, want_p)]
+    q_out = torch.zeros_like(want_q)
+    ws = cvq.paged_workspace_alloc(a[0], cvq.paged_suggest_splits(a[0]), "cuda")
+    wp = cvq.prefix_workspace_alloc(shape, cvq.prefix_suggest_splits(shape, x.dtype), "cuda")
+    torch.cuda.synchronize()
+    cvq.paged_attend(*a, workspace=ws, out=outs[0][0], lse=outs[0][1], stream=st)
+    prefix(workspace=wp, out=outs[1][0], lse=outs[1][1], stream=st)
+    cvq.paged_append(pg, k, v, off, lens, table, kp, vp, q=q, q_out=q_out, stream=st)
+    st.synchronize()
+    for got, w in zip(outs, (want, want_p)):
+        assert torch.equal(got[0], w[0]) and torch.equal(got[1], w[1])
+    assert torch.equal(q_out[:43], want_q[:43])
