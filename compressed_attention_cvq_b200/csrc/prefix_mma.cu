@@ -735,6 +735,8 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, 1) prefix_mma_kernel(c
                                       ((static_cast<size_t>(h) * C + rank) * 2 + (kKeys ? 0 : 1)) * (static_cast<size_t>(rounds) * kWideCodes * 128) + cl * 16;
       const float* far_cb = (kKeys ? a.key_cb + static_cast<long long>(h) * a.key_cb_stride : a.val_cb + static_cast<long long>(h) * a.val_cb_stride) +
                             static_cast<size_t>(rank) * rounds * kWideCodes * 64 + cl * 8;
+      constexpr int kUnroll = kWide ? 1 : 2;      // both stages, where the body is short
+#pragma unroll kUnroll
       for (int i = 0; i < ntiles; ++i) {
         const int s = kStages == 2 ? i & 1 : 0, lap = i / kStages;
         auto stage_free = [&] { return lap == 0 || wait(empty + s, (lap - 1) & 1, a.fault); };

@@ -532,3 +532,58 @@ def test_the_stream_argument():
     for got, w in zip(outs, (want, want_p)):
         assert torch.equal(got[0], w[0]) and torch.equal(got[1], w[1])
     assert torch.equal(q_out[:43], want_q[:43])
+
+
+def test_tensors_that_do_not_fit_are_refused():
+    """Every wrong tensor of the three calls is a ValueError that names it, before any launch."""
+    import compressed_attention_cvq_b200 as cvq
+    pg, q, kp, vp, table, lens = setup([40, 3], 8, 2, 16, "bf16", "bf16", seed=1)
+    ws = cvq.paged_workspace_alloc(pg, 2, "cuda")
+    state = (torch.zeros(2, 8, 128, device="cuda"), torch.zeros(2, 8, device="cuda"))
+    base = dict(q=q, k_pages=kp, v_pages=vp, page_table=table, seq_lens=lens, n_splits=2,
+                workspace=ws, prev=state)
+    bad = [dict(q=q.cpu()), dict(q=q[:1]), dict(q=q.double()), dict(q=q.transpose(0, 1)),
+           dict(q=q.expand(2, 8, 128)[:, :, :64]), dict(k_pages=kp.half()), dict(v_pages=vp[:-1]),
+           dict(k_pages=kp.transpose(1, 2)), dict(v_pages=vp.cpu()), dict(page_table=table.long()),
+           dict(page_table=table[:, :1].contiguous()), dict(page_table=table.t().contiguous().t()),
+           dict(seq_lens=lens[:1]), dict(seq_lens=lens.float()), dict(workspace=ws[:100]),
+           dict(workspace=ws.cpu()), dict(n_splits=0), dict(n_splits=5000),
+           dict(prev=(state[0].half(), state[1])), dict(prev=(state[0], state[1][:, :4])),
+           dict(prev=(state[0].cpu(), state[1])), dict(out=q.float()[:1]), dict(lse=state[1].double()),
+           dict(out=state[0], out_dtype=torch.bfloat16), dict(out_dtype=torch.float64)]
+    for kw in bad:
+        with pytest.raises(ValueError):
+            cvq.paged_attend(pg, **{**base, **kw})
+    for kw in (dict(q=None), dict(k_pages=3), dict(out_dtype="bf16")):
+        with pytest.raises(TypeError):
+            cvq.paged_attend(pg, **{**base, **kw})
+    apg, aq, k, v, off, al, at, akp, avp = append_case([3, 4], [0, 2], 8, 2, 16, "bf16", "bf16")
+    base = dict(k=k, v=v, tok_offsets=off, seq_lens=al, page_table=at, k_pages=akp, v_pages=avp, q=aq)
+    before = akp.clone()
+    for kw in [dict(k=k.cpu()), dict(k=k.double()), dict(v=v.float()), dict(v=v[:3]), dict(q=aq[:, :4]),
+               dict(q=aq.half()), dict(k=k[:, :, ::2]), dict(q=aq.transpose(1, 2)),
+               dict(tok_offsets=off[:2]), dict(tok_offsets=off.long()), dict(seq_lens=al.cpu()),
+               dict(pos_offsets=al[:1]), dict(pos_offsets=al.float()), dict(q_out=aq.float()),
+               dict(q_out=aq[:3]), dict(q=None, q_out=aq), dict(k_pages=akp.half()), dict(k=k[0])]:
+        with pytest.raises(ValueError):
+            cvq.paged_append(apg, **{**base, **kw})
+    odd = torch.zeros(7 * (256 + 4), dtype=torch.bfloat16, device="cuda").as_strided((7, 2, 128), (260, 128, 1))
+    with pytest.raises(cvq.CvqError):                        # a token stride of 520 bytes
+        cvq.paged_append(apg, **{**base, "k": odd})
+    assert torch.equal(akp, before)
+    d = workloads.small(batch=1, n_q_heads=8, n_kv_heads=2, t_cap=640, R=2, seed=4)
+    dev = {n: torch.from_numpy(d[n]).cuda() for n in ("key_cb", "val_cb", "key_codes", "val_codes")}
+    x = torch.randn(4, 8, 128, device="cuda").bfloat16()
+    shape = cvq.shape_of(x, dev["key_codes"])
+    base = dict(q=x, prefix_len=i32([600]), **dev)
+    for kw in [dict(q=x.cpu()), dict(q=x[:3]), dict(q=x.double()), dict(prefix_len=i32([6, 6])),
+               dict(prefix_len=i32([6]).long()), dict(key_cb=dev["key_cb"].half()),
+               dict(key_cb=dev["val_cb"]), dict(val_cb=dev["key_cb"]), dict(key_cb=dev["key_cb"][:1]),
+               dict(key_codes=dev["key_codes"][:, :, :639]), dict(val_codes=dev["val_codes"].int()),
+               dict(val_codes=dev["val_codes"].cpu()), dict(key_codes=dev["key_codes"].transpose(2, 3)),
+               dict(n_splits=0), dict(workspace=torch.zeros(16, dtype=torch.uint8, device="cuda")),
+               dict(out=x.float()[:2]), dict(out_dtype=torch.int8)]:
+        with pytest.raises(ValueError):
+            cvq.prefix_attend(shape, **{**base, **kw})
+    cvq.prefix_attend(shape, **base)
+    assert cvq.fault_status(clear=True) == 0
