@@ -11,14 +11,18 @@
 // remainders -- a query or weight x is split as hi = 16-bit(x), lo = 16-bit(x - hi), and the two
 // result rows are added.  So fp32 queries, queries of the other 16-bit type and the softmax
 // weights keep 16 bits (bf16 pages) or 22 bits (fp16 pages) at no extra instruction, since a
-// group has at most 8 heads.  For fp16 pages a query row is first scaled by a power of two
-// into fp16's range, and the weights are taken relative to 2^15 below the maximum, so that the
-// small ones stay normal numbers.  bf16 has fp32's range: there they are taken relative to 2^-8, so
-// that sums of the largest values have room (the weights' sum, relative to the maximum, may reach
-// 2^136 over the largest value).  Scores, weights' sums and outputs accumulate in fp32.
+// group has at most 8 heads.  Where queries or outputs are fp32 and a group has at most 4 heads
+// (kFine), the rows that are left, 4-7, take a third part (24 bits), and a warp adds its outputs to
+// an fp32 copy in shared memory every 64 chunks, since the accumulators of the matrix instructions
+// do not round to nearest: over 16384 tokens outputs are off by 1.0e-6 instead of 4.0e-6 (fp32
+// arithmetic 1.7e-6) at 494 us instead of 485.
+// For fp16 pages a query row is first scaled by a power of two into fp16's range, and the weights
+// are taken relative to 2^15 below the maximum, so that the small ones stay normal numbers.  bf16
+// has fp32's range: there they are taken relative to 2^-8, so that sums of the largest values have
+// room.  Scores, weights' sums and outputs accumulate in fp32.
 //
-// Measured in a captured graph, 8 KV heads, bf16 pages: 64 sequences of up to 16384 tokens 486 us
-// (6.6 TB/s, the rate of a copy), one of 131071 (fp16) 89 us (6.0 TB/s), 16 of 1024 to 8192 54 us
+// Measured in a captured graph, 8 KV heads, bf16 pages: 64 sequences of up to 16384 tokens 494 us
+// (6.5 TB/s, the rate of a copy; fp32 queries), one of 131071 (fp16) 89 us (6.0 TB/s), 16 of 1024 to 8192 54 us
 // (5.7 TB/s), 32 of up to 128 7.2 us.
 //
 // Split: a CTA of 4 warps takes one (sequence, KV head, run of tokens); a warp
@@ -44,6 +48,7 @@ constexpr int kRowBytes = 2 * kHeadDim;
 constexpr int kTileBytes = kChunk * kRowBytes;    // keys or values of a stage
 constexpr int kRingBytes = kStages * 2 * kTileBytes;
 constexpr int kSmemBytes = kWarps * kRingBytes;
+constexpr int kRun = 64;                          // chunks between flushes of a warp's outputs (kFine)
 constexpr int kCtasPerSm = 2;                     // 96 KB of ring each
 static_assert(kRingBytes >= 8 * kHeadDim * 4, "a warp's output fits its ring");
 
@@ -71,22 +76,22 @@ __device__ __forceinline__ void mma16<__half>(float (&c)[4], const uint32_t (&a)
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// x and y as a pair of 16-bit numbers, and the pair of their remainders
+// x and y as a pair of 16-bit numbers; x and y become their remainders
 template <typename T>
-__device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo);
+__device__ __forceinline__ uint32_t take_part(float& x, float& y);
 template <>
-__device__ __forceinline__ void split2<__nv_bfloat16>(float x, float y, uint32_t& hi, uint32_t& lo) {
+__device__ __forceinline__ uint32_t take_part<__nv_bfloat16>(float& x, float& y) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
-  const __nv_bfloat162 l = __floats2bfloat162_rn(x - __low2float(h), y - __high2float(h));
-  hi = *reinterpret_cast<const uint32_t*>(&h);
-  lo = *reinterpret_cast<const uint32_t*>(&l);
+  x -= __low2float(h);
+  y -= __high2float(h);
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
 template <>
-__device__ __forceinline__ void split2<__half>(float x, float y, uint32_t& hi, uint32_t& lo) {
+__device__ __forceinline__ uint32_t take_part<__half>(float& x, float& y) {
   const __half2 h = __floats2half2_rn(x, y);
-  const __half2 l = __floats2half2_rn(x - __low2float(h), y - __high2float(h));
-  hi = *reinterpret_cast<const uint32_t*>(&h);
-  lo = *reinterpret_cast<const uint32_t*>(&l);
+  x -= __low2float(h);
+  y -= __high2float(h);
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 // out and lse of one row from its sum (M in log2 units, L, and lane's 4 dims of o), with the
@@ -112,7 +117,7 @@ __device__ __forceinline__ void finish_row(const ServeArgs& a, size_t row, int l
   if (lane == 0) a.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;
 }
 
-template <typename T>
+template <typename T, bool kFine>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attend_kernel(const __grid_constant__ ServeArgs a) {
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ uint32_t s_mask[kWarps][kStages];
@@ -120,7 +125,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attend_kernel(cons
   __shared__ int s_last, s_longest[kWarps];
   static_assert(kWarps == 4, "the maximum below");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int gid = lane >> 2, tid = lane & 3;      // fragment row (head) and column pair
+  const int gid = lane >> 2, tid = lane & 3;      // fragment row and column pair
+  const int head = kFine ? gid & 3 : gid;         // of the group
+  const bool upper = kFine && gid >= 4;           // rows with the third parts
   const int split = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   int L = a.lens[b];
@@ -190,19 +197,32 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attend_kernel(cons
     page = next;
   }
 
+  // the parts of x and y that belong in this lane's rows: gid, and gid + 8
+  auto parts = [&](float x, float y, uint32_t& low_row, uint32_t& high_row) {
+    low_row = take_part<T>(x, y);
+    high_row = take_part<T>(x, y);
+    if constexpr (kFine) {
+      const uint32_t third = take_part<T>(x, y);
+      if (upper) {
+        low_row = third;
+        high_row = 0u;
+      }
+    }
+  };
+
   // ---- the query operand ----
   uint32_t qa[8][4];
   float factor = 0.08838834764831845f * kLog2e;   // of a product of the operand rows
   {
     float x[8][4];
-    const size_t at = (row0 + gid) * kHeadDim;
+    const size_t at = (row0 + head) * kHeadDim;
     float mx = 0.f;
 #pragma unroll
     for (int kt = 0; kt < 8; ++kt) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int d = kt * 16 + 2 * tid + (j & 1) + (j >> 1) * 8;
-        x[kt][j] = gid < a.group ? load_any(a.q, a.q_dtype, at + d) : 0.f;
+        x[kt][j] = head < a.group ? load_any(a.q, a.q_dtype, at + d) : 0.f;
         mx = fmaxf(mx, fabsf(x[kt][j]));
       }
     }
@@ -219,8 +239,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attend_kernel(cons
     }
 #pragma unroll
     for (int kt = 0; kt < 8; ++kt) {
-      split2<T>(x[kt][0] * down, x[kt][1] * down, qa[kt][0], qa[kt][1]);
-      split2<T>(x[kt][2] * down, x[kt][3] * down, qa[kt][2], qa[kt][3]);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float u = x[kt][2 * j] * down, v = x[kt][2 * j + 1] * down;
+        parts(u, v, qa[kt][2 * j], qa[kt][2 * j + 1]);
+      }
     }
   }
 
@@ -233,6 +256,30 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attend_kernel(cons
   for (int n = 0; n < 16; ++n)
 #pragma unroll
     for (int j = 0; j < 4; ++j) o[n][j] = 0.f;
+  // kFine: this lane's outputs so far, added in fp32 and taken to the maximum of now
+  float* kept = reinterpret_cast<float*>(smem + kSmemBytes) + warp * (4 * kHeadDim);
+  float m_kept = -INFINITY;
+  int run = 0;
+  bool any = false;
+  auto flush = [&] {
+    const float f = m_kept == -INFINITY ? 0.f : exp2f(m_kept - m);
+#pragma unroll
+    for (int n = 0; n < 16; ++n) {
+      float u = o[n][0] + o[n][2], v = o[n][1] + o[n][3];
+      u += __shfl_xor_sync(0xffffffffu, u, 16);
+      v += __shfl_xor_sync(0xffffffffu, v, 16);
+      if (!upper) {
+        float2* at = reinterpret_cast<float2*>(kept + gid * kHeadDim + 8 * n + 2 * tid);
+        const float2 x = any ? *at : make_float2(0.f, 0.f);
+        *at = make_float2(fmaf(x.x, f, u), fmaf(x.y, f, v));
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) o[n][j] = 0.f;
+    }
+    m_kept = m;
+    run = 0;
+    any = true;
+  };
   for (int i = warp; i < nchunks; i += kWarps) {
     const int ahead = i + (kStages - 1) * kWarps;
     const int next = load_page(ahead + kWarps);
@@ -262,7 +309,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attend_kernel(cons
     for (int n = 0; n < 2; ++n)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        s[n][j] = (c[n][j] + c[n][j + 2]) * factor;
+        s[n][j] = c[n][j] + c[n][j + 2];
+        if (kFine) s[n][j] += __shfl_xor_sync(0xffffffffu, s[n][j], 16);
+        s[n][j] *= factor;
         if (mask != 0xffffu && !((mask >> (8 * n + 2 * tid + j)) & 1u)) s[n][j] = -INFINITY;
       }
     float mx = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
@@ -288,8 +337,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attend_kernel(cons
         l += p[n][j];
       }
     uint32_t pa[4];
-    split2<T>(p[0][0], p[0][1], pa[0], pa[1]);
-    split2<T>(p[1][0], p[1][1], pa[2], pa[3]);
+    parts(p[0][0], p[0][1], pa[0], pa[1]);
+    parts(p[1][0], p[1][1], pa[2], pa[3]);
     {
       const int r = (lane & 7) + (((lane >> 3) & 1) << 3), sel = lane >> 4;
 #pragma unroll
@@ -301,6 +350,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attend_kernel(cons
       }
     }
     __syncwarp();                                 // the stage may be refilled
+    if constexpr (kFine) {
+      if (++run == kRun) flush();
+    }
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
   l += __shfl_xor_sync(0xffffffffu, l, 1);
@@ -308,11 +360,18 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attend_kernel(cons
   __syncwarp();
 
   // ---- join the warps: each leaves [8 heads][128] and its maximum and sum ----
-  float* mine = reinterpret_cast<float*>(smem + warp * kRingBytes);
+  if constexpr (kFine) {
+    flush();
+  } else {
+    float* mine = reinterpret_cast<float*>(smem + warp * kRingBytes);
 #pragma unroll
-  for (int n = 0; n < 16; ++n)
-    *reinterpret_cast<float2*>(mine + gid * kHeadDim + 8 * n + 2 * tid) =
-        make_float2(o[n][0] + o[n][2], o[n][1] + o[n][3]);
+    for (int n = 0; n < 16; ++n)
+      *reinterpret_cast<float2*>(mine + gid * kHeadDim + 8 * n + 2 * tid) =
+          make_float2(o[n][0] + o[n][2], o[n][1] + o[n][3]);
+  }
+  auto left_by = [&](int w) {
+    return reinterpret_cast<const float*>(kFine ? smem + kSmemBytes + w * (4 * kHeadDim * 4) : smem + w * kRingBytes);
+  };
   if (tid == 0) {
     s_m[warp][gid] = m == -INFINITY ? -INFINITY : m - kLift;
     s_l[warp][gid] = l;
@@ -328,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attend_kernel(cons
     for (int w = 0; w < kWarps; ++w) {
       if (s_m[w][r] == -INFINITY && s_l[w][r] == 0.f) continue;             // no token
       const float f = exp2f(s_m[w][r] - M);
-      const float4 x = *reinterpret_cast<const float4*>(smem + w * kRingBytes + (r * kHeadDim + 4 * lane) * 4);
+      const float4 x = *reinterpret_cast<const float4*>(left_by(w) + r * kHeadDim + 4 * lane);
       sum = fmaf(s_l[w][r], f, sum);
       acc = make_float4(fmaf(x.x, f, acc.x), fmaf(x.y, f, acc.y), fmaf(x.z, f, acc.z), fmaf(x.w, f, acc.w));
     }
@@ -421,18 +480,21 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attend_kernel(cons
   if (threadIdx.x == 0) atomicExch(counter, 0);
 }
 
-template <typename T>
+template <typename T, bool kFine>
 cudaError_t run(const ServeArgs& a, cudaStream_t stream) {
   static PerDeviceFlag flag;
-  const cudaError_t e = set_smem_limit_once(flag, paged_attend_kernel<T>, kSmemBytes);
+  constexpr size_t bytes = kSmemBytes + (kFine ? kWarps * 4 * kHeadDim * sizeof(float) : 0);
+  const cudaError_t e = set_smem_limit_once(flag, paged_attend_kernel<T, kFine>, bytes);
   if (e != cudaSuccess) return e;
-  return launch_chained(paged_attend_kernel<T>, dim3(a.n_splits, a.n_kv_heads, a.batch), kThreads, a, stream, kSmemBytes);
+  return launch_chained(paged_attend_kernel<T, kFine>, dim3(a.n_splits, a.n_kv_heads, a.batch), kThreads, a, stream, bytes);
 }
 
 }  // namespace
 
 cudaError_t launch_paged_attend(const ServeArgs& a, cudaStream_t stream) {
-  return a.kv_dtype == CVQ_BF16 ? run<__nv_bfloat16>(a, stream) : run<__half>(a, stream);
+  const bool fine = a.group <= 4 && (a.q_dtype == CVQ_F32 || a.out_dtype == CVQ_F32);
+  if (a.kv_dtype == CVQ_BF16) return fine ? run<__nv_bfloat16, true>(a, stream) : run<__nv_bfloat16, false>(a, stream);
+  return fine ? run<__half, true>(a, stream) : run<__half, false>(a, stream);
 }
 
 }  // namespace cvq

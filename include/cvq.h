@@ -464,7 +464,8 @@ CVQ_API cvq_status cvq_paged_append(const cvq_paged* paged, int32_t n_tokens, co
  *   A sequence is split into shares of the longest sequence of the call, of 256 tokens or more.
  *   Arithmetic: products are 16-bit, of operands split in two 16-bit numbers where they are not
  *   exact (queries of another type than the pages', softmax weights: 2^-17 relative over bf16
- *   pages, 2^-22 over fp16 pages); sums are kept in fp32.
+ *   pages, 2^-22 over fp16 pages), and in three for fp32 queries or outputs with Hq/Hkv <= 4;
+ *   sums are kept in fp32.
  * ------------------------------------------------------------------------------- */
 CVQ_API size_t cvq_paged_workspace_bytes(const cvq_paged* paged, int n_splits);
 /* A split count for sequences of up to max_pages * page_size tokens (a suggestion). */

@@ -587,3 +587,19 @@ def test_tensors_that_do_not_fit_are_refused():
             cvq.prefix_attend(shape, **{**base, **kw})
     cvq.prefix_attend(shape, **base)
     assert cvq.fault_status(clear=True) == 0
+
+
+@pytest.mark.parametrize("cache,Hq,bound", [("bf16", 8, 3e-6), ("fp16", 8, 3e-6), ("bf16", 2, 3e-6)])
+def test_fp32_outputs_over_long_sequences(cache, Hq, bound):
+    """Relative to the result's norm: operands in three parts are off by 2^-24 each (fp16 pages, two:
+    2^-22), sums of 64 chunks in the accumulators by at most 64 x 2^-23 x 1/2 of their own size
+    on average, and those sums, taken every 64 chunks, by one rounding: below 64 x 2^-24 = 3.8e-6
+    at the worst, and less as the accumulators start from nothing (half of it) and the errors of
+    128 dims and 4 warps are not all of one sign (3e-6 leaves room for the scores' 2^-22 x |s|)."""
+    import compressed_attention_cvq_b200 as cvq
+    a = setup([30000, 9000, 70], Hq, 2, 32, "fp32", cache, seed=8)
+    out, lse = cvq.paged_attend(*a)
+    ref = U.paged_reference(np64(a[1]), np64(a[2]), np64(a[3]), a[4].cpu().numpy(), a[5].tolist())
+    for b in range(3):
+        assert np.linalg.norm(np64(out)[b] - ref[0][b]) <= bound * np.linalg.norm(ref[0][b])
+        assert np.abs(np64(lse)[b] - ref[1][b]).max() <= 1e-6 * np.abs(ref[1][b]).max()
