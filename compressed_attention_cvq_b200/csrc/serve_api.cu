@@ -32,11 +32,14 @@ size_t round16(size_t n) { return (n + 15) / 16 * 16; }
 // CTAs of the tensor-core kernel that share a split (each leaves a partial state)
 int prefix_pair(const cvq_shape* s) { return !is_wide(s) && s->R == 1 ? 1 : 2; }
 
-// Whether the tensor-core kernel takes the call: 16-bit queries and room for 512 tokens.  Its scores are off by 2^-11 each, which averages out over a
-// softmax (lse of 512 tokens: 5e-6 relative) but not over a few tokens (64: 2e-5); and a prefix
-// that short takes either kernel the same time, that of the launches.
+// Whether the tensor-core kernel takes the call: 16-bit queries over 2048 tokens, or over 512 with
+// 65536 scores in all.  Its scores are off by 2^-11 each, which averages out over a
+// softmax (lse of 512 tokens: 5e-6 relative) but not over a few tokens (64: 2e-5); and fewer scores
+// take either kernel about the same time, that of the launches (1000 tokens: 4 sequences 10.9 us in
+// fp32 and 12.7 here, 16 sequences 19.6 and 15.5).
 bool prefix_on_tensor_cores(const cvq_shape* s, int q_dtype) {
-  return q_dtype != CVQ_F32 && s->t_cap >= 512;
+  const int64_t scores = static_cast<int64_t>(s->t_cap) * s->batch * s->n_q_heads;
+  return q_dtype != CVQ_F32 && (s->t_cap >= 2048 || (s->t_cap >= 512 && scores >= 65536));
 }
 
 // partial states of (sequence, query head) rows, 16-byte aligned

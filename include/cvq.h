@@ -366,7 +366,8 @@ CVQ_API cvq_status cvq_attend_static(const cvq_shape* shape, const void* q, int 
  *              workspace must be ordered on one stream
  *   out        [B, Hq, 128] of out_dtype (fp32, bf16 or fp16), 16-byte aligned
  *   lse        [B, Hq] fp32, natural log
- *   Arithmetic: fp32 queries and caches of t_cap < 512 are multiplied in fp32.  The
+ *   Arithmetic: fp32 queries are multiplied in fp32, and so are caches of t_cap < 512
+ *              and, below t_cap = 2048, calls of fewer than 65536 scores (t_cap * B * Hq).  The
  *              other 16-bit queries are multiplied on the tensor cores as fp16: codewords, sums
  *              of two rounds' codewords (group_dim 64 sums those in fp32), the sines, the rotated key, the value
  *              and the softmax weights are rounded to fp16 (2^-11 at most each), codebooks

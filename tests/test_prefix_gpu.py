@@ -257,11 +257,12 @@ def test_head_offsets_past_32_bits(dtype):
 
 @pytest.mark.parametrize("group,R,bits", [(8, 1, 0), (8, 2, 0), (64, 1, 8), (64, 4, 6), (64, 11, 8)])
 @pytest.mark.parametrize("length", [0, 1, 63, 64, 65, 127, 129, 192, 513, 640])
-def test_short_prefixes_in_a_larger_cache(group, R, bits, length):
-    """Lengths around the tiles of 64 and the pairs' steps of 128 tokens, in a cache with room for
-    640, as one split and as several."""
+@pytest.mark.parametrize("cap", [640, 2048])         # in fp32, and on the tensor cores
+def test_short_prefixes_in_a_larger_cache(group, R, bits, length, cap):
+    """Lengths around the tiles of 64 and the pairs' steps of 128 tokens, in a cache with more
+    room, as one split and as several."""
     import compressed_attention_cvq_b200 as cvq
-    d, dev = make(5, 8, 2, 640, R, "fp16", group, seed=R + length)
+    d, dev = make(5, 8, 2, cap, R, "fp16", group, seed=R + length)
     codes = None
     if bits == 6:
         shape = cvq.shape_of(dev["q"][:1], dev["key_codes"], group_dim=64)
@@ -275,19 +276,21 @@ def test_short_prefixes_in_a_larger_cache(group, R, bits, length):
 @pytest.mark.parametrize("B,g", [(31, 4), (32, 4), (33, 4), (128, 1), (129, 1), (32, 8), (1, 8)])
 @pytest.mark.parametrize("R", [1, 2])
 def test_row_counts_around_a_block(B, g, R):
-    """124 to 258 rows of a KV head: a block holds 128."""
+    """124 to 258 rows of a KV head, and 8: a block holds 128."""
     import compressed_attention_cvq_b200 as cvq
-    d, dev = make(B, 2 * g, 2, 700, R, "bf16", seed=B + R)
-    verify(d, call(cvq, dev, 690), 690, "bf16")
+    for cap in (700, 2050):
+        d, dev = make(B, 2 * g, 2, cap, R, "bf16", seed=B + R)
+        verify(d, call(cvq, dev, 690), 690, "bf16")
 
 
 @pytest.mark.parametrize("group,R", [(8, 1), (8, 2), (64, 3), (64, 11)])
 @pytest.mark.parametrize("k_scale,v_scale", [(2.0 ** 20, 1.0), (2.0 ** -30, 2.0 ** -40), (1.0, 2.0 ** 60),
                                              (2.0 ** 12, 2.0 ** 110)])
-def test_codebooks_far_from_one(group, R, k_scale, v_scale):
+@pytest.mark.parametrize("cap", [640, 2048])
+def test_codebooks_far_from_one(group, R, k_scale, v_scale, cap):
     """Codebooks that leave fp16's range as they are; the queries take the keys' scale back."""
     import compressed_attention_cvq_b200 as cvq
-    d, dev = make(4, 8, 2, 640, R, "bf16", group, seed=R)
+    d, dev = make(4, 8, 2, cap, R, "bf16", group, seed=R)
     for name, f in (("key_cb", k_scale), ("val_cb", v_scale)):
         d[name] = (d[name] * np.float32(f)).astype(np.float32)
         dev[name] = torch.from_numpy(d[name]).cuda()
@@ -299,17 +302,18 @@ def test_codebooks_far_from_one(group, R, k_scale, v_scale):
     verify(d, (got[0].double() / v_scale, got[1]), 600, "bf16", "fp32")
 
 
-def test_queries_far_from_one():
+@pytest.mark.parametrize("cap", [640, 2048])
+def test_queries_far_from_one(cap):
     import compressed_attention_cvq_b200 as cvq
     for f in (2.0 ** -100, 2.0 ** 90):
-        d, dev = make(3, 8, 2, 640, 2, "bf16", seed=2)
+        d, dev = make(3, 8, 2, cap, 2, "bf16", seed=2)
         d["key_cb"] = (d["key_cb"] / np.float32(f)).astype(np.float32)
         dev["key_cb"] = torch.from_numpy(d["key_cb"]).cuda()
         dev["q"] = (dev["q"].double() * f).bfloat16()
         d["q"] = dev["q"].double().cpu().numpy()
         verify(d, call(cvq, dev, 640), 640, "bf16")
     # a row of zeros attends evenly; a row that is not finite leaves the others alone
-    d, dev = make(3, 8, 2, 640, 2, "bf16", seed=3)
+    d, dev = make(3, 8, 2, cap, 2, "bf16", seed=3)
     want = call(cvq, dev, 640)
     dev["q"][0, 1] = 0
     dev["q"][1, 5, 7] = float("nan")
@@ -323,9 +327,10 @@ def test_queries_far_from_one():
 
 
 @pytest.mark.parametrize("R,dtype,bits", [(12, "bf16", 6), (22, "fp16", 8), (21, "fp32", 6)])
-def test_many_rounds(R, dtype, bits):
+@pytest.mark.parametrize("cap", [640, 2048])
+def test_many_rounds(R, dtype, bits, cap):
     import compressed_attention_cvq_b200 as cvq
-    d, dev = make(6, 8, 2, 640, R, dtype, 64, seed=R)
+    d, dev = make(6, 8, 2, cap, R, dtype, 64, seed=R)
     codes = None
     if bits == 6:
         shape = cvq.shape_of(dev["q"][:1], dev["key_codes"], group_dim=64)
@@ -348,7 +353,7 @@ def test_rounds_beyond_the_held_ones(R, scale):
     """More rounds than a pair of SMs holds: the others come from the workspace's copy, or, where
     their scale is not the usual one, from the codebooks."""
     import compressed_attention_cvq_b200 as cvq
-    d, dev = make(7, 8, 2, 1024, R, "fp16", 64, seed=R)
+    d, dev = make(7, 8, 2, 2048, R, "fp16", 64, seed=R)
     for name in ("key_cb", "val_cb"):
         d[name] = (d[name] * np.float32(scale)).astype(np.float32)
         dev[name] = torch.from_numpy(d[name]).cuda()
@@ -361,4 +366,59 @@ def test_rounds_beyond_the_held_ones(R, scale):
     got = call(cvq, dev, 1000, 64, 0, 2, out_dtype=torch.float32)
     d["val_cb"] = d["val_cb"] / scale
     verify(d, (got[0].double() / scale, got[1]), 1000, "fp16", "fp32")
+    assert cvq.fault_status(clear=True) == 0
+
+
+@pytest.mark.parametrize("R", [1, 2])
+def test_the_tensor_cores_calls(R):
+    """What the tests above ask of small caches in fp32, of a cache large enough for the tensor
+    cores: one codebook for all heads, one code for all tokens, what lies behind the prefix, sharp
+    scores, streams and graphs with one workspace, any output type and split count."""
+    import compressed_attention_cvq_b200 as cvq
+    d, dev = make(10, 8, 2, 2100, R, "bf16", shared=True, seed=3)
+    verify(d, call(cvq, dev, 2100), 2100, "bf16")
+    for k in ("key_codes", "val_codes"):
+        d[k][:] = 255
+        dev[k].fill_(255)
+    verify(d, call(cvq, dev, 2100), 2100, "bf16", seen_codes=1)
+    d, dev = make(4, 8, 2, 2500, R, "bf16", seed=6, std=7.0)
+    verify(d, call(cvq, dev, 2500), 2500, "bf16")
+    d, dev = make(8, 8, 2, 2400, R, "bf16", seed=4)
+    for k in ("key_codes", "val_codes"):
+        d[k][d[k] == 0] = 1
+        dev[k].copy_(torch.from_numpy(d[k]))
+    shape = cvq.shape_of(dev["q"], dev["key_codes"])
+    n = cvq.prefix_suggest_splits(shape, torch.bfloat16)
+    ln = torch.tensor([1777], dtype=torch.int32, device="cuda")
+    ws = [cvq.prefix_workspace_alloc(shape, n, "cuda") for _ in range(2)]
+
+    def go(w, **kw):
+        return cvq.prefix_attend(shape, dev["q"], dev["key_cb"], dev["key_codes"], dev["val_codes"],
+                                 ln, dev["val_cb"], n, workspace=w, **kw)
+    want = go(ws[0])
+    dev["key_cb"][:, :, :, 0] = float("nan")
+    dev["val_cb"][:, :, :, 0] = float("inf")
+    for k in ("key_codes", "val_codes"):
+        dev[k][:, :, 1777:] = 0
+    torch.cuda.synchronize()
+    got = []
+    for w in ws:                                             # two calls at once
+        st = torch.cuda.Stream()
+        with torch.cuda.stream(st):
+            got.append(go(w))
+    torch.cuda.synchronize()
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got.append(go(ws[0]))
+        graphs.append(g)
+    for g in graphs + graphs:
+        g.replay()
+    torch.cuda.synchronize()
+    for o, z in got:
+        assert torch.equal(o, want[0]) and torch.equal(z, want[1])
+    for od in ("fp32", "fp16"):
+        for k in (1, 3, 4096):
+            verify(d, call(cvq, dev, 1777, n_splits=k, out_dtype=DT[od]), 1777, "bf16", od)
     assert cvq.fault_status(clear=True) == 0
