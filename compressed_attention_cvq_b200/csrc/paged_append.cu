@@ -5,10 +5,10 @@
 // few tokens.  All its threads first load their chunk of a row (16 bytes: 8 dims of 16-bit input, 4 of
 // fp32); under these loads two warps find the token's sequence and row and take
 // the sine and cosine of a pair a lane; one barrier, and the rows are rotated and stored.  Many
-// small CTAs with one chunk a thread in flight measured best: 8192 tokens of 32 + 16 heads in bf16 take
-// 42 us (4.8 TB/s; a copy of the same bytes by the framework 67), with 256 threads 45, with three
-// chunks a thread 56, a warp a token without a barrier 63; 1531 tokens of fp32 8.6 us (7.0 TB/s, some
-// of it from L2), a decode step of 32 tokens 2.5 us.
+// small CTAs with two chunks a thread in flight measured best: 8192 tokens of 32 + 16 heads in bf16 take
+// 40 us (5.1 TB/s; a copy of the same bytes by the framework 67), with one chunk 42, with 256 threads
+// more, a warp a token without a barrier 63; 1531 tokens of fp32 8.7 us (some of it from L2; 12.3 from
+// memory), a decode step of 32 tokens 2.5 us.
 #include <algorithm>
 
 #include "serve.cuh"
@@ -55,7 +55,7 @@ __global__ void __launch_bounds__(kThreads, 12) paged_append_kernel(const __grid
   const int stride = gridDim.y * kSlots;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   Chunk<In, kD> in;
-  auto load = [&](int r) {
+  auto load = [&](int r, Chunk<In, kD>& in) {
     if (r < heads) {
       const In* src = r < nq ? static_cast<const In*>(a.q) + i * a.q_stride + r * kHeadDim
                     : r < nk ? static_cast<const In*>(a.k) + i * a.k_stride + (r - nq) * kHeadDim
@@ -64,7 +64,7 @@ __global__ void __launch_bounds__(kThreads, 12) paged_append_kernel(const __grid
     }
   };
   int r = blockIdx.y * kSlots + threadIdx.x / kLanes;
-  load(r);
+  load(r, in);
   if (warp < kPairs / 32) {
     // the sequence: as many as end at or before i (offsets do not decrease); 32 probes at a time
     int b = 0, n = a.batch;
@@ -106,6 +106,8 @@ __global__ void __launch_bounds__(kThreads, 12) paged_append_kernel(const __grid
 #pragma unroll
   for (int v = 0; v < kD / 4; ++v) ph[v] = s_ph[c * (kD / 4) + v];
   while (r < heads) {
+    Chunk<In, kD> next;                                    // under this one's arithmetic
+    load(r + stride, next);
     float x[kD];
 #pragma unroll
     for (int d = 0; d < kD; ++d) x[d] = to_float(in.x[d]);
@@ -132,7 +134,7 @@ __global__ void __launch_bounds__(kThreads, 12) paged_append_kernel(const __grid
       *reinterpret_cast<Chunk<Kv, kD>*>(pool + at + (static_cast<long long>(h) << a.page_shift) * kHeadDim + kD * c) = out;
     }
     r += stride;
-    load(r);
+    in = next;
   }
 }
 
