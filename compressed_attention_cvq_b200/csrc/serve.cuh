@@ -19,7 +19,7 @@ struct ServeArgs {
   int q_dtype;
   int batch, n_q_heads, n_kv_heads, group;
   int n_splits;
-  int n_parts;                    // partial states per row: n_splits, or one per CTA of its pairs
+  int n_parts;                    // partial states per row: n_splits, or one per CTA of their clusters
   float* part_o;
   float* part_m;
   float* part_l;
@@ -40,8 +40,9 @@ struct ServeArgs {
   const uint8_t* val_codes;
   int R, wide, code_bits;
   PhaseTurns phase;
-  void* book;                     // codebooks in fp16, as the tensor-core kernel holds them
+  void* book;                     // codebooks in the tensor-core kernel's order
   uint32_t* book_peak;            // their largest elements
+  float* kept_o;                  // [row][part][2][128], sums of long streams
   // paged cache
   const void* k_pages;
   const void* v_pages;

@@ -30,16 +30,16 @@ bool is_wide(const cvq_shape* s) { return s->group_dim == kWideGroupDim; }
 size_t round16(size_t n) { return (n + 15) / 16 * 16; }
 
 // CTAs of the tensor-core kernel that share a split (each leaves a partial state)
-int prefix_pair(const cvq_shape* s) { return !is_wide(s) && s->R == 1 ? 1 : 2; }
+int prefix_cluster(const cvq_shape* s) { return !is_wide(s) && s->R == 1 ? 2 : 4; }
 
-// Whether the tensor-core kernel takes the call: 16-bit queries over 2048 tokens, or over 512 with
-// 65536 scores in all.  Its scores are off by 2^-11 each, which averages out over a
-// softmax (lse of 512 tokens: 5e-6 relative) but not over a few tokens (64: 2e-5); and fewer scores
-// take either kernel about the same time, that of the launches (1000 tokens: 4 sequences 10.9 us in
-// fp32 and 12.7 here, 16 sequences 19.6 and 15.5).
+// Whether the tensor-core kernel takes the call: 16-bit queries, where it is the faster one (both
+// hold what fp32 holds).  The other takes 64 rows of a KV head at a time and has less to set up.
+// 8 KV heads, R = 1, us in fp32 and here: 1000 tokens of 1, 4, 16, 32 sequences of 4 heads a group
+// 11.1 16.1, 11.2 16.4, 17.9 18.7, 33.6 23.2; 2000 tokens of 1, 4, 8, 16 16.4 16.9, 16.9 17.3, 30.6 18.5,
+// 31.9 19.5; 192 tokens of 64 21.7 25.3.
 bool prefix_on_tensor_cores(const cvq_shape* s, int q_dtype) {
-  const int64_t scores = static_cast<int64_t>(s->t_cap) * s->batch * s->n_q_heads;
-  return q_dtype != CVQ_F32 && (s->t_cap >= 2048 || (s->t_cap >= 512 && scores >= 65536));
+  const int64_t rows = static_cast<int64_t>(s->batch) * (s->n_q_heads / s->n_kv_heads);
+  return q_dtype != CVQ_F32 && (s->t_cap >= 2048 || (s->t_cap >= 512 && rows > 64));
 }
 
 // partial states of (sequence, query head) rows, 16-byte aligned
@@ -47,10 +47,15 @@ size_t parts_bytes(int batch, int n_q_heads, int n_parts) {
   return round16(static_cast<size_t>(batch) * n_q_heads * n_parts * (kHeadDim + 2) * sizeof(float));
 }
 
-// both codebooks of every KV head in fp16
+// what long streams of the tensor-core kernel have summed: two outputs a row and CTA
+size_t kept_bytes(int batch, int n_q_heads, int n_parts) {
+  return static_cast<size_t>(batch) * n_q_heads * n_parts * 2 * kHeadDim * sizeof(float);
+}
+
+// both codebooks of every KV head
 size_t book_bytes(const cvq_shape* s) {
   const size_t entries = is_wide(s) ? kWideGroups * kWideCodes * kWideGroupDim : kGroups * kCodes * kCodeword;
-  return 2 * static_cast<size_t>(s->n_kv_heads) * s->R * entries * sizeof(uint16_t);
+  return 2 * static_cast<size_t>(s->n_kv_heads) * s->R * entries * sizeof(float);
 }
 
 void place_parts(ServeArgs& a, void* workspace) {
@@ -103,22 +108,21 @@ extern "C" {
 
 size_t cvq_prefix_workspace_bytes(const cvq_shape* s, int n_splits) {
   if (cvq_partials_bytes(s, n_splits) == 0) return 0;
-  // the book's items of 16 bytes leave one peak per 256
-  return parts_bytes(s->batch, s->n_q_heads, n_splits * prefix_pair(s)) + book_bytes(s) + round16(book_bytes(s) / 1024);
+  // the books' items of 16 bytes leave one peak per 256; two streams a CTA keep an output each
+  const int parts = n_splits * prefix_cluster(s);
+  return parts_bytes(s->batch, s->n_q_heads, parts) + book_bytes(s) + round16(book_bytes(s) / 1024) + kept_bytes(s->batch, s->n_q_heads, parts);
 }
 
 int cvq_prefix_suggest_splits(const cvq_shape* s, int q_dtype, int sm_count) {
   if (cvq_partials_bytes(s, 1) == 0 || sm_count < 1 || !is_dtype(q_dtype)) return 1;
   const long long rows = static_cast<long long>(s->batch) * (s->n_q_heads / s->n_kv_heads);
   if (prefix_on_tensor_cores(s, q_dtype)) {
-    // One CTA per SM, and of pairs those that fit at once (72 on 148 SMs).  A split of single CTAs
-    // holds a tile of 64 tokens; one of pairs, which have more to set up, two of each CTA, and four
-    // beyond 16 splits (12345 tokens of 2 KV heads: 25 splits 17.4 us, 33 splits 19.0)
-    const int pair = prefix_pair(s);
-    const long long ctas = static_cast<long long>(s->n_kv_heads) * ((rows + 127) / 128) * pair;
-    const long long tiles = (static_cast<long long>(s->t_cap) + 63) / 64;
-    const long long most = pair == 1 ? tiles : std::max((tiles + 7) / 8, std::min((tiles + 3) / 4, 16LL));
-    return static_cast<int>(std::max(1LL, std::min({4096LL, most, (pair == 1 ? sm_count : sm_count - 4) / ctas})));
+    // clusters that fit at once (of 148 SMs 72 pairs, 33 of four), and two steps or more for each
+    const int size = prefix_cluster(s);
+    const long long units = static_cast<long long>(s->n_kv_heads) * ((rows + 127) / 128);
+    const long long fit = size == 2 ? (sm_count - 4) / 2 : sm_count / 4 - 4;
+    const long long steps = (static_cast<long long>(s->t_cap) + 64 * size - 1) / (64 * size);
+    return static_cast<int>(std::max(1LL, std::min({4096LL, (steps + 1) / 2, fit / units})));
   }
   const long long units = s->n_kv_heads * (rows <= 16 ? 1 : (rows + 63) / 64);
   const long long tiles = std::max(1LL, (static_cast<long long>(s->t_cap) + 63) / 64);
@@ -155,7 +159,7 @@ cvq_status cvq_prefix_attend(const cvq_shape* s, const void* q, int q_dtype, con
   a.group = s->n_q_heads / s->n_kv_heads;
   const bool tensor = prefix_on_tensor_cores(s, q_dtype);
   a.n_splits = n_splits;
-  a.n_parts = tensor ? n_splits * prefix_pair(s) : n_splits;
+  a.n_parts = tensor ? n_splits * prefix_cluster(s) : n_splits;
   a.lens = prefix_len;
   a.t_cap = s->t_cap;
   a.out = out;
@@ -175,6 +179,7 @@ cvq_status cvq_prefix_attend(const cvq_shape* s, const void* q, int q_dtype, con
   char* rest = static_cast<char*>(workspace) + parts_bytes(a.batch, a.n_q_heads, a.n_parts);
   a.book = rest;
   a.book_peak = reinterpret_cast<uint32_t*>(rest + book_bytes(s));
+  a.kept_o = reinterpret_cast<float*>(rest + book_bytes(s) + round16(book_bytes(s) / 1024));
   if (fault_word_address(&a.fault) != cudaSuccess) return CVQ_ERR_CUDA;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   CVQ_TRY(from_cuda(tensor ? launch_prefix_mma(a, st) : launch_prefix_f32(a, st)));

@@ -348,7 +348,8 @@ CVQ_API cvq_status cvq_attend_static(const cvq_shape* shape, const void* q, int 
 /* ---------------------------------------------------------------------------------
  * cvq_prefix_attend -- one decode step of a whole batch against ONE compressed prefix
  * that every sequence shares (a system prompt, a document), computed once for all: each
- * cached token is decoded once per KV head and read by the query heads of every sequence.
+ * cached token is decoded once per KV head and block of 128 query rows (64 in fp32; a row is a
+ * sequence and one of its query heads of that KV head), and read by all rows of the block.
  *   For sequence b and query head hq, with h = hq / (Hq / Hkv), the formulas of the top of
  *   this file over the tokens t = 0..L-1 of the one cache, L = prefix_len[0].  Fold the
  *   state of each sequence's own tokens in with cvq_paged_attend.
@@ -366,13 +367,14 @@ CVQ_API cvq_status cvq_attend_static(const cvq_shape* shape, const void* q, int 
  *              workspace must be ordered on one stream
  *   out        [B, Hq, 128] of out_dtype (fp32, bf16 or fp16), 16-byte aligned
  *   lse        [B, Hq] fp32, natural log
- *   Arithmetic: fp32 queries are multiplied in fp32, and so are caches of t_cap < 512
- *              and, below t_cap = 2048, calls of fewer than 65536 scores (t_cap * B * Hq).  The
- *              other 16-bit queries are multiplied on the tensor cores as fp16: codewords, sums
- *              of two rounds' codewords (group_dim 64 sums those in fp32), the sines, the rotated key, the value
- *              and the softmax weights are rounded to fp16 (2^-11 at most each), codebooks
- *              and query rows scaled by powers of two into its range; sums of products, the
- *              softmax and the merge are kept in fp32
+ *   Arithmetic: as exact as fp32 (out within a few 1e-6 of its scale, lse within 1e-6), whatever
+ *              the queries' type.  fp32 queries are multiplied in fp32, and so are small calls of
+ *              16-bit queries (t_cap < 512, or t_cap < 2048 with at most 64 query rows per KV head).
+ *              The others are multiplied on the tensor cores: 16-bit queries as they are, decoded
+ *              keys and values and the softmax weights as two fp16 numbers each (22 bits), the
+ *              codebooks and query rows scaled by powers of two into fp16's range; sums of codewords,
+ *              rotations, sums of products, the softmax and the merge are fp32.  An output whose
+ *              weighted codewords are not all finite is not finite
  *   Errors as in cvq_attend.
  * ------------------------------------------------------------------------------- */
 CVQ_API size_t cvq_prefix_workspace_bytes(const cvq_shape* shape, int n_splits);
