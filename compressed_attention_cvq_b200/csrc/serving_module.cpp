@@ -96,20 +96,24 @@ c10::Device cuda_device(const at::Tensor& t, const char* name) {
   return t.device();
 }
 
-// The library launches on the current device: the tensors' own, for as long as this lives.
-struct OnDevice {
-  explicit OnDevice(c10::Device dev) {
-    if (c10::cuda::current_device() != dev.index()) guard.set_index(dev.index());
+// The tensors' device is current, and so is the stream that a call was given: for as long as this
+// lives.  The library launches on the current device; what the call allocates, and clears, for itself
+// is then ordered with its kernels, and the allocator hands it on in the order of the same stream.
+struct On {
+  On(c10::Device dev, PyObject* given) {
+    if (given == Py_None) {
+      if (c10::cuda::current_device() != dev.index()) device.set_index(dev.index());
+    } else {
+      void* p = PyLong_AsVoidPtr(given);
+      if (p == nullptr && PyErr_Occurred()) throw python_error();
+      current.reset_stream(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(p), dev.index()));
+    }
+    stream = c10::cuda::getCurrentCUDAStream(dev.index()).stream();
   }
-  c10::cuda::OptionalCUDAGuard guard;
+  c10::cuda::OptionalCUDAGuard device;
+  c10::cuda::OptionalCUDAStreamGuard current;
+  void* stream;
 };
-
-void* stream_of(PyObject* stream, c10::Device dev) {
-  if (stream == Py_None) return c10::cuda::getCurrentCUDAStream(dev.index()).stream();
-  void* p = PyLong_AsVoidPtr(stream);
-  if (p == nullptr && PyErr_Occurred()) throw python_error();
-  return p;
-}
 
 int sm_count(c10::Device dev) {
   int n = 0;
@@ -244,13 +248,13 @@ PyObject* prefix_attend(PyObject*, PyObject* const* p, Py_ssize_t n) {
   check(len, "prefix_len", dev, at::kInt, {1});
   const int64_t ks = codebook_stride(kcb, "key_cb", dev, s, true), vs = codebook_stride(vcb, "val_cb", dev, s, false);
   const int qd = dtype_code(q.scalar_type(), "q");
-  const OnDevice on(dev);
+  const On on(dev, p[12]);
   const int splits = p[7] == Py_None ? api.prefix_suggest_splits(s, qd, sm_count(dev)) : int_of(p[7]);
   const at::Tensor ws = workspace_of(p[8], api.prefix_workspace_bytes(s, splits), dev, "cvq_prefix_workspace_bytes");
   const Outputs o = outputs_of(p[9], p[10], p[11], q.scalar_type(), s->batch, s->n_q_heads, dev);
   raise_for(api.prefix_attend(s, ptr(q), qd, ptr<float>(kcb), ks, ptr<uint8_t>(kc), ptr<uint8_t>(vc),
                               ptr<int32_t>(len), ptr<float>(vcb), vs, splits, ptr(ws), ptr(o.out),
-                              dtype_code(o.out.scalar_type(), "out"), ptr<float>(o.lse), stream_of(p[12], dev)),
+                              dtype_code(o.out.scalar_type(), "out"), ptr<float>(o.lse), on.stream),
             "cvq_prefix_attend");
   return result(o, p[9], p[10]);
   END_HANDLE_TH_ERRORS
@@ -293,6 +297,7 @@ PyObject* paged_append(PyObject*, PyObject* const* p, Py_ssize_t n_args) {
   const at::Tensor &k = tensor(p[1], "k"), &v = tensor(p[2], "v"), &off = tensor(p[3], "tok_offsets"), &lens = tensor(p[4], "seq_lens"),
                    &table = tensor(p[5], "page_table"), &kp = tensor(p[6], "k_pages"), &vp = tensor(p[7], "v_pages");
   const c10::Device dev = cuda_device(k, "k");
+  const On on(dev, p[11]);
   if (k.dim() != 3 || k.size(0) > INT32_MAX) bad("k must be [tokens, KV heads, 128]");
   const int64_t n = k.size(0);
   const at::ScalarType dt = k.scalar_type();
@@ -323,10 +328,9 @@ PyObject* paged_append(PyObject*, PyObject* const* p, Py_ssize_t n_args) {
   }
   const int code = dtype_code(dt, "k");
   if (n > 0) {
-    const OnDevice on(dev);
     raise_for(api.paged_append(g, static_cast<int32_t>(n), q, qs, ptr(k), ks, ptr(v), vs, code, ptr<int32_t>(off),
                                ptr<int32_t>(lens), pos, ptr<int32_t>(table), ptr(kp), ptr(vp),
-                               q != nullptr ? ptr(qo) : nullptr, stream_of(p[11], dev)),
+                               q != nullptr ? ptr(qo) : nullptr, on.stream),
               "cvq_paged_append");
   }
   if (p[9] != Py_None || p[8] == Py_None) return Py_NewRef(p[9]);
@@ -354,13 +358,13 @@ PyObject* paged_attend(PyObject*, PyObject* const* p, Py_ssize_t n) {
     pl = ptr<float>(b);
   }
   const int qd = dtype_code(q.scalar_type(), "q");
-  const OnDevice on(dev);
+  const On on(dev, p[13]);
   const int splits = p[6] == Py_None ? api.paged_suggest_splits(g, sm_count(dev)) : int_of(p[6]);
   const at::Tensor ws = workspace_of(p[7], api.paged_workspace_bytes(g, splits), dev, "cvq_paged_workspace_bytes");
   const Outputs o = outputs_of(p[10], p[11], p[12], q.scalar_type(), g->batch, g->n_q_heads, dev);
   raise_for(api.paged_attend(g, ptr(q), qd, ptr(kp), ptr(vp), ptr<int32_t>(table), ptr<int32_t>(lens),
                              splits, ptr(ws), po, pl, ptr(o.out), dtype_code(o.out.scalar_type(), "out"),
-                             ptr<float>(o.lse), stream_of(p[13], dev)),
+                             ptr<float>(o.lse), on.stream),
             "cvq_paged_attend");
   return result(o, p[10], p[11]);
   END_HANDLE_TH_ERRORS

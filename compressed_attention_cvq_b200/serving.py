@@ -13,7 +13,8 @@ One decode step of a batch behind a shared prefix:
 
 Tensors are checked against the shapes that the library is told (it gets plain pointers), in
 native code (csrc/serving_module.cpp): wrong devices, types, shapes and strides are ValueErrors.
-Work is enqueued on the current CUDA stream of the tensors' device.
+Work is enqueued on the current CUDA stream of the tensors' device, or on `stream`: then as if it
+were the current one, so that outputs and workspaces which the call allocates are that stream's too.
 """
 from __future__ import annotations
 
