@@ -69,6 +69,13 @@ def _workspace(need, dev, what):
     return torch.zeros(need, dtype=torch.uint8, device=dev)
 
 
+def _at(struct, kind):
+    """Address of a shape, whose type the native side cannot see."""
+    if not isinstance(struct, kind):
+        raise TypeError(f"expected a {kind.__name__}, got {type(struct).__name__}")
+    return addressof(struct)
+
+
 def _raw(stream):
     return None if stream is None else stream.cuda_stream
 
@@ -90,7 +97,7 @@ def prefix_attend(shape, q, key_cb, key_codes, val_codes, prefix_len, val_cb, n_
     over ONE code cache key_codes / val_codes [(1,) Hkv, t_cap, R, 16] (64-scalar groups:
     planar [(1,) Hkv, 2, R, t_cap], packed 3 t_cap / 4) of prefix_len [1] int32 tokens.
     Returns (out [B, Hq, 128] of out_dtype, default q's type, and lse [B, Hq] fp32)."""
-    return _native.prefix_attend(addressof(shape), q, key_cb, key_codes, val_codes, prefix_len,
+    return _native.prefix_attend(_at(shape, _b.cvq_shape), q, key_cb, key_codes, val_codes, prefix_len,
                                  val_cb, n_splits, workspace, out, lse, out_dtype, _raw(stream))
 
 
@@ -119,7 +126,7 @@ def paged_append(paged, k, v, tok_offsets, seq_lens, page_table, k_pages, v_page
     whose lengths seq_lens [B] already count them; token i belongs to sequence b for
     tok_offsets[b] <= i < tok_offsets[b+1].  Its RoPE position is pos_offsets[b] (or 0) plus
     its index in the sequence.  q [n, Hq, 128], if given, is rotated into q_out (returned)."""
-    return _native.paged_append(addressof(paged), k, v, tok_offsets, seq_lens, page_table,
+    return _native.paged_append(_at(paged, _b.cvq_paged), k, v, tok_offsets, seq_lens, page_table,
                                 k_pages, v_pages, q, q_out, pos_offsets, _raw(stream))
 
 
@@ -129,6 +136,6 @@ def paged_attend(paged, q, k_pages, v_pages, page_table, seq_lens, n_splits=None
     its seq_lens[b] tokens; prev = (out, lse) in fp32 of an earlier part of the sequences
     (prefix_attend, attend_fused) is merged in.  Returns (out, lse) as prefix_attend."""
     prev_out, prev_lse = (None, None) if prev is None else prev
-    return _native.paged_attend(addressof(paged), q, k_pages, v_pages, page_table, seq_lens,
+    return _native.paged_attend(_at(paged, _b.cvq_paged), q, k_pages, v_pages, page_table, seq_lens,
                                 n_splits, workspace, prev_out, prev_lse, out, lse, out_dtype,
                                 _raw(stream))
