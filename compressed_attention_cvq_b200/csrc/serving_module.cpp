@@ -217,7 +217,7 @@ int64_t codebook_stride(const at::Tensor& cb, const char* name, c10::Device dev,
     if (per_head) check(cb, name, dev, at::kFloat, {H, groups, s->R, entries, d});
     else check(cb, name, dev, at::kFloat, {groups, s->R, entries, d});
   }
-  return per_head ? cb.numel() / H : 0;
+  return per_head ? groups * s->R * entries * d : 0;
 }
 
 void check_codes(const at::Tensor& t, const char* name, c10::Device dev, const cvq_shape* s) {
