@@ -281,12 +281,13 @@ void check_pages(const cvq_paged* g, const at::Tensor& kp, const at::Tensor& vp,
   check(lens, "seq_lens", dev, at::kInt, {g->batch});
 }
 
-// token stride of [n, heads, 128] whose heads are dense (tokens may be strided)
+// token stride of [n, heads, 128] whose heads are dense (tokens may be strided; a single one has no
+// stride, whatever the tensor says)
 int64_t token_stride(const at::Tensor& t, const char* name, c10::Device dev, at::ScalarType dtype, int64_t n, int64_t heads) {
   if (t.device() != dev || t.scalar_type() != dtype) bad(std::string(name) + " must be " + dtype_name(dtype) + " on " + dev.str());
   if (!same(t.sizes(), {n, heads, 128}) || t.stride(2) != 1 || (heads > 1 && t.stride(1) != 128))
     bad(std::string(name) + " must be [" + std::to_string(n) + ", " + std::to_string(heads) + ", 128] with dense heads");
-  return n > 1 ? t.stride(0) : std::max(t.stride(0), heads * 128);
+  return n > 1 ? t.stride(0) : heads * 128;
 }
 
 // paged, k, v, tok_offsets, seq_lens, page_table, k_pages, v_pages, q, q_out, pos_offsets, stream
