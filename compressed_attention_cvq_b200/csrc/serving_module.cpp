@@ -351,7 +351,7 @@ PyObject* paged_attend(PyObject*, PyObject* const* p, Py_ssize_t n) {
   check(q, "q", dev, q.scalar_type(), {g->batch, g->n_q_heads, 128});
   check_pages(g, kp, vp, table, lens, dev);
   const float *po = nullptr, *pl = nullptr;
-  if (p[8] != Py_None) {
+  if (p[8] != Py_None || p[9] != Py_None) {
     const at::Tensor &a = tensor(p[8], "prev out"), &b = tensor(p[9], "prev lse");
     check(a, "prev out", dev, at::kFloat, {g->batch, g->n_q_heads, 128});
     check(b, "prev lse", dev, at::kFloat, {g->batch, g->n_q_heads});

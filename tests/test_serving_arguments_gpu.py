@@ -39,3 +39,16 @@ def test_one_token_of_a_fused_projection():
         kp.zero_()
         got = cvq.paged_append(pg, k, v, *args, q=q, q_out=q, pos_offsets=first)
         assert got is q and torch.equal(q, want) and torch.equal(kp, pages)
+
+
+def test_half_a_state_is_refused():
+    import compressed_attention_cvq_b200 as cvq
+    pg = cvq.make_paged(1, 8, 2, 16, 4, 4)
+    kp, vp = (torch.zeros((4, 2, 16, 128), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    q = torch.zeros((1, 8, 128), dtype=torch.bfloat16, device="cuda")
+    args = (pg, q, kp, vp, i32([[0, 1, 2, 3]]), i32([5]))
+    o, z = torch.zeros((1, 8, 128), device="cuda"), torch.zeros((1, 8), device="cuda")
+    for prev in ((None, z), (o, None)):
+        with pytest.raises(TypeError, match="prev"):
+            cvq.paged_attend(*args, prev=prev)
+    cvq.paged_attend(*args, prev=(o, z))
