@@ -42,6 +42,12 @@ bool prefix_on_tensor_cores(const cvq_shape* s, int q_dtype) {
   return q_dtype != CVQ_F32 && (s->t_cap >= 2048 || (s->t_cap >= 512 && rows > 64));
 }
 
+// A workspace starts with the arrival counters of paged calls, one per (sequence, KV head), at a
+// place that no call's states reach, whatever its shape: so every paged call finds them as the last one
+// left them, at zero.  Calls of more units than that have CTAs enough without splits.
+constexpr int kCounters = 16384;
+constexpr size_t kCounterBytes = kCounters * sizeof(int);
+
 // partial states of (sequence, query head) rows, 16-byte aligned
 size_t parts_bytes(int batch, int n_q_heads, int n_parts) {
   return round16(static_cast<size_t>(batch) * n_q_heads * n_parts * (kHeadDim + 2) * sizeof(float));
@@ -60,7 +66,7 @@ size_t book_bytes(const cvq_shape* s) {
 
 void place_parts(ServeArgs& a, void* workspace) {
   const size_t rows = static_cast<size_t>(a.batch) * a.n_q_heads * a.n_parts;
-  a.part_o = static_cast<float*>(workspace);
+  a.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + kCounterBytes);
   a.part_m = a.part_o + rows * kHeadDim;
   a.part_l = a.part_m + rows;
 }
@@ -110,7 +116,7 @@ size_t cvq_prefix_workspace_bytes(const cvq_shape* s, int n_splits) {
   if (cvq_partials_bytes(s, n_splits) == 0) return 0;
   // the books' items of 16 bytes leave one peak per 256; two streams a CTA keep an output each
   const int parts = n_splits * prefix_cluster(s);
-  return parts_bytes(s->batch, s->n_q_heads, parts) + book_bytes(s) + round16(book_bytes(s) / 1024) + kept_bytes(s->batch, s->n_q_heads, parts);
+  return kCounterBytes + parts_bytes(s->batch, s->n_q_heads, parts) + book_bytes(s) + round16(book_bytes(s) / 1024) + kept_bytes(s->batch, s->n_q_heads, parts);
 }
 
 int cvq_prefix_suggest_splits(const cvq_shape* s, int q_dtype, int sm_count) {
@@ -176,7 +182,7 @@ cvq_status cvq_prefix_attend(const cvq_shape* s, const void* q, int q_dtype, con
   a.code_bits = s->code_bits == 6 ? 6 : 8;
   phase_turns_host(s->rope_base, &a.phase);
   place_parts(a, workspace);
-  char* rest = static_cast<char*>(workspace) + parts_bytes(a.batch, a.n_q_heads, a.n_parts);
+  char* rest = static_cast<char*>(workspace) + kCounterBytes + parts_bytes(a.batch, a.n_q_heads, a.n_parts);
   a.book = rest;
   a.book_peak = reinterpret_cast<uint32_t*>(rest + book_bytes(s));
   a.kept_o = reinterpret_cast<float*>(rest + book_bytes(s) + round16(book_bytes(s) / 1024));
@@ -188,8 +194,7 @@ cvq_status cvq_prefix_attend(const cvq_shape* s, const void* q, int q_dtype, con
 
 size_t cvq_paged_workspace_bytes(const cvq_paged* p, int n_splits) {
   if (check_paged(p) != CVQ_OK || n_splits < 1 || n_splits > 4096) return 0;
-  // and one arrival counter per (sequence, KV head)
-  return parts_bytes(p->batch, p->n_q_heads, n_splits) + round16(static_cast<size_t>(p->batch) * p->n_kv_heads * sizeof(int));
+  return kCounterBytes + parts_bytes(p->batch, p->n_q_heads, n_splits);
 }
 
 int cvq_paged_suggest_splits(const cvq_paged* p, int sm_count) {
@@ -295,7 +300,7 @@ cvq_status cvq_paged_attend(const cvq_paged* p, const void* q, int q_dtype, cons
   a.n_q_heads = p->n_q_heads;
   a.n_kv_heads = p->n_kv_heads;
   a.group = p->n_q_heads / p->n_kv_heads;
-  a.n_splits = a.n_parts = n_splits;
+  a.n_splits = a.n_parts = static_cast<int64_t>(p->batch) * p->n_kv_heads > kCounters ? 1 : n_splits;
   a.t_cap = p->max_pages * p->page_size;
   a.lens = seq_lens;
   a.prev_out = prev_out;
@@ -312,7 +317,7 @@ cvq_status cvq_paged_attend(const cvq_paged* p, const void* q, int q_dtype, cons
   a.max_pages = p->max_pages;
   a.page_stride = stride_of(p);
   place_parts(a, workspace);
-  a.counters = reinterpret_cast<int*>(static_cast<char*>(workspace) + parts_bytes(a.batch, a.n_q_heads, n_splits));
+  a.counters = static_cast<int*>(workspace);
   if (fault_word_address(&a.fault) != cudaSuccess) return CVQ_ERR_CUDA;
   return from_cuda(launch_paged_attend(a, static_cast<cudaStream_t>(stream)));
 }

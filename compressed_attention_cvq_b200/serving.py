@@ -115,7 +115,8 @@ def paged_suggest_splits(paged, sm_count=None):
 
 
 def paged_workspace_alloc(paged, n_splits, device):
-    """Zeroed workspace for paged_attend (every call leaves it ready for the next)."""
+    """Zeroed workspace for paged_attend.  Every call leaves it ready for the next, of any shape
+    and split count that it has room for; prefix_attend may use it in between."""
     return _workspace(_b.lib.cvq_paged_workspace_bytes(ctypes.byref(paged), n_splits), device,
                       "cvq_paged_workspace_bytes")
 

@@ -362,8 +362,8 @@ CVQ_API cvq_status cvq_attend_static(const cvq_shape* shape, const void* q, int 
  *   key_codes, val_codes  the cache of one sequence: [Hkv, t_cap, R, 16], or planar
  *              [Hkv, 2, R, t_cap] (packed [Hkv, 2, R, 3 t_cap / 4])
  *   prefix_len [1] int32 (device), clamped to [0, t_cap]; 0: out = 0, lse = -inf
- *   workspace  cvq_prefix_workspace_bytes(shape, n_splits) bytes, 16-byte aligned; its
- *              contents before and after a call are of no meaning.  Calls that share a
+ *   workspace  cvq_prefix_workspace_bytes(shape, n_splits) bytes or more, 16-byte aligned; its
+ *              contents before and after a call are of no meaning to it.  Calls that share a
  *              workspace must be ordered on one stream
  *   out        [B, Hq, 128] of out_dtype (fp32, bf16 or fp16), 16-byte aligned
  *   lse        [B, Hq] fp32, natural log
@@ -456,15 +456,16 @@ CVQ_API cvq_status cvq_paged_append(const cvq_paged* paged, int32_t n_tokens, co
  *   q          [B, Hq, 128] fp32, bf16 or fp16, rotated (q_out of cvq_paged_append)
  *   prev_out   [B, Hq, 128] fp32, prev_lse [B, Hq] fp32, both or neither NULL; they may be
  *              out (when fp32) and lse themselves
- *   workspace  cvq_paged_workspace_bytes(paged, n_splits) bytes, 16-byte aligned, with the
- *              rules of cvq_attend's: zero when the first call starts; a call leaves what
- *              the next call of the same shape and n_splits needs; calls that share one are
- *              ordered on one stream
+ *   workspace  cvq_paged_workspace_bytes(paged, n_splits) bytes or more, 16-byte aligned: zero
+ *              when the first call starts; a call leaves what the next one needs, whatever
+ *              its shape and n_splits.  Calls of cvq_prefix_attend may use it in between.  Calls
+ *              that share one are ordered on one stream
  *   out, lse   as in cvq_prefix_attend
  *   A page index outside [0, n_pages) is not followed: its tokens count as absent, and
  *   CVQ_PAGE_FAULT is set in the fault word.  Rows behind seq_lens[b] are not read, whatever
  *   they hold.
- *   A sequence is split into shares of the longest sequence of the call, of 256 tokens or more.
+ *   A sequence is split into shares of the longest sequence of the call, of 256 tokens or more
+ *   (not split where B * Hkv > 16384).
  *   Arithmetic: products are 16-bit, of operands split in two 16-bit numbers where they are not
  *   exact (queries of another type than the pages', softmax weights: 2^-17 relative over bf16
  *   pages, 2^-22 over fp16 pages), and in three for fp32 queries or outputs with Hq/Hkv <= 4;
