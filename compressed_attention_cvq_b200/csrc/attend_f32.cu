@@ -53,7 +53,7 @@ __device__ __forceinline__ void decode_side(const ServeArgs& a, const float* cb,
     int code[kPer * kR];
 #pragma unroll
     for (int j = 0; j < kPer * kR; ++j) {
-      const int t = min(t0 + tk + j / kR * kStep, end - 1);
+      const int t = t0 + min(tk + j / kR * kStep, end - 1 - t0);       // t0 + 64 may pass 32 bits
       code[j] = __ldg(codes + ((static_cast<size_t>(h) * a.t_cap + t) * kR + j % kR) * kGroups + c);
     }
 #pragma unroll
@@ -64,7 +64,7 @@ __device__ __forceinline__ void decode_side(const ServeArgs& a, const float* cb,
       const float* book = cb + (static_cast<size_t>(G) * a.R + r) * (kWideCodes * kWideGroupDim) + 8 * (c & 7);
 #pragma unroll
       for (int u = 0; u < kPer; ++u)
-        add8(x[u], book + wide_code(codes, a, h, G, r, min(t0 + tk + u * kStep, end - 1)) * kWideGroupDim);
+        add8(x[u], book + wide_code(codes, a, h, G, r, t0 + min(tk + u * kStep, end - 1 - t0)) * kWideGroupDim);
     }
   }
 }
@@ -81,7 +81,7 @@ __device__ __forceinline__ void make_tile(const ServeArgs& a, const unsigned lon
   float2 ph[4], step[4];
 #pragma unroll
   for (int p = 0; p < 4; ++p) {
-    ph[p] = phase_exact(f_tab[4 * c + p] * static_cast<unsigned long long>(static_cast<unsigned>(t0 + tk)));
+    ph[p] = phase_exact(f_tab[4 * c + p] * static_cast<unsigned long long>(static_cast<unsigned>(t0) + tk));
     step[p] = phase_exact(f_tab[4 * c + p] * kStep);
   }
 #pragma unroll
@@ -92,7 +92,7 @@ __device__ __forceinline__ void make_tile(const ServeArgs& a, const unsigned lon
       for (int p = 0; p < 4; ++p)
         ph[p] = make_float2(ph[p].x * step[p].x - ph[p].y * step[p].y, ph[p].x * step[p].y + ph[p].y * step[p].x);
     }
-    const bool in = t0 + row < end;
+    const bool in = row < end - t0;
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
       const float re = x[u][2 * p], im = x[u][2 * p + 1];
@@ -105,7 +105,7 @@ __device__ __forceinline__ void make_tile(const ServeArgs& a, const unsigned lon
 #pragma unroll
   for (int u = 0; u < kPer; ++u) {
     const int row = tk + u * kStep;
-    if (t0 + row >= end) {
+    if (row >= end - t0) {
 #pragma unroll
       for (int d = 0; d < 8; ++d) x[u][d] = 0.f;
     }
@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(kThreads, RB == 16 || kWide ? 2 : 1) attend_f3
   const int r0 = blockIdx.z * RB;
   int L = a.lens[0];
   L = L < 0 ? 0 : (L > a.t_cap ? a.t_cap : L);
-  const long long per = ((L + a.n_splits - 1LL) / a.n_splits + kTile - 1) / kTile * kTile;
+  const long long per = ((static_cast<long long>(L) + a.n_splits - 1) / a.n_splits + kTile - 1) / kTile * kTile;
   const int start = static_cast<int>(min(per * split, static_cast<long long>(L)));
   const int end = static_cast<int>(min(start + per, static_cast<long long>(L)));
   // global row (sequence, query head) of local row r
@@ -192,12 +192,14 @@ __global__ void __launch_bounds__(kThreads, RB == 16 || kWide ? 2 : 1) attend_f3
 #pragma unroll
     for (int d = 0; d < 8; ++d) o[i][d] = 0.f;
   }
-  for (int t0 = start; t0 < end; t0 += kTile) {
+  const int ntiles = static_cast<int>((static_cast<long long>(end) - start + kTile - 1) / kTile);
+  for (int i = 0; i < ntiles; ++i) {
+    const int t0 = start + i * kTile;
     __syncthreads();                                // the last tile's readers are done
     if constexpr (kWide) make_tile<0>(a, f_tab, h, t0, end, sk, sv);
     else if (a.R == 1) make_tile<1>(a, f_tab, h, t0, end, sk, sv);
     else make_tile<2>(a, f_tab, h, t0, end, sk, sv);
-    if (RB == 16 && t0 == start) put_query(tid, early);
+    if (RB == 16 && i == 0) put_query(tid, early);
     __syncthreads();
     float s[RPT][4];
 #pragma unroll
@@ -236,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, RB == 16 || kWide ? 2 : 1) attend_f3
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      if (t0 + tx + 16 * j >= end) {
+      if (tx + 16 * j >= end - t0) {
 #pragma unroll
         for (int i = 0; i < RPT; ++i) s[i][j] = -INFINITY;
       }

@@ -83,7 +83,7 @@ __device__ __forceinline__ float load_q(const void* q, int q_dtype, size_t idx) 
 // byte (j = 0, 3) or two bytes of its own 3-byte group (j = 1, 2); nothing past the
 // group is read.
 __device__ __forceinline__ int packed6_code(const uint8_t* row, int t) {
-  const int bit = 6 * t, by = bit >> 3, sh = bit & 7;
+  const int bit = 6 * (t & 3), by = (t >> 2) * 3 + (bit >> 3), sh = bit & 7;      // 6 t passes 32 bits
   uint32_t w = row[by];
   if (sh > 2) w |= static_cast<uint32_t>(row[by + 1]) << 8;
   return static_cast<int>((w >> sh) & 63u);

@@ -144,10 +144,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attend_kernel(cons
     __syncthreads();
     longest = min(max(max(s_longest[0], s_longest[1]), max(s_longest[2], s_longest[3])), a.t_cap);
   }
-  const long long share = (longest + a.n_splits - 1LL) / a.n_splits;
+  const long long share = (static_cast<long long>(longest) + a.n_splits - 1) / a.n_splits;
   const long long per64 = max(static_cast<long long>(kMinSplit), (share + kSplitAlign - 1) / kSplitAlign * kSplitAlign);
-  const int per = static_cast<int>(min(per64, 0x7fffffc0LL));
-  const int used = L == 0 ? 1 : static_cast<int>((L + per - 1LL) / per);     // splits that hold tokens
+  const int per = static_cast<int>(min(per64, 0x7fffffffLL));               // one split holds any length
+  const int used = L == 0 ? 1 : static_cast<int>((static_cast<long long>(L) + per - 1) / per);     // splits that hold tokens
   if (split >= used) return;
   const int start = split * per;                  // < L
   const int end = min(L - start, per) + start;
@@ -158,17 +158,19 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attend_kernel(cons
   const int* table = a.page_table + static_cast<size_t>(b) * a.max_pages;
   const uint32_t ring = smem_u32(smem) + warp * kRingBytes;
   const int slot_mask = (1 << a.page_shift) - 1;
-  // page of token lane & 15 of chunk i, loaded one chunk ahead of its use
+  // token lane & 15 of chunk i (a chunk may pass 2^31 where the sequence ends just before), and its
+  // page, loaded one chunk ahead of its use
+  auto token = [&](int i) { return static_cast<unsigned>(start) + static_cast<unsigned>(i) * kChunk + (lane & 15); };
   auto load_page = [&](int i) {
-    const int t = start + i * kChunk + (lane & 15);
-    return i < nchunks && t < end ? __ldg(table + (t >> a.page_shift)) : 0;
+    const unsigned t = token(i);
+    return i < nchunks && t < static_cast<unsigned>(end) ? __ldg(table + (t >> a.page_shift)) : 0;
   };
   auto issue = [&](int i, int page) {
     if (i < nchunks) {
-      const int t = start + i * kChunk + (lane & 15);
+      const unsigned t = token(i);
       const bool in_range = static_cast<unsigned>(page) < static_cast<unsigned>(a.n_pages);
-      const bool have = t < end && in_range;
-      if (t < end && !in_range) atomicOr(a.fault, kFaultPage);
+      const bool mine = t < static_cast<unsigned>(end), have = mine && in_range;
+      if (mine && !in_range) atomicOr(a.fault, kFaultPage);
       const uint32_t mask = __ballot_sync(0xffffffffu, have) & 0xffffu;
       const long long off = have ? static_cast<long long>(page) * a.page_stride +
                                        (static_cast<long long>(h) * (slot_mask + 1) + (t & slot_mask)) * kHeadDim

@@ -389,7 +389,7 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, 1) prefix_mma_kernel(c
   };
   int L = a.lens[0];
   L = L < 0 ? 0 : (L > a.t_cap ? a.t_cap : L);
-  const long long per = ((L + a.n_splits - 1LL) / a.n_splits + kGroupTok - 1) / kGroupTok * kGroupTok;
+  const long long per = ((static_cast<long long>(L) + a.n_splits - 1) / a.n_splits + kGroupTok - 1) / kGroupTok * kGroupTok;
   const long long start = min(per * split, static_cast<long long>(L)), end = min(start + per, static_cast<long long>(L));
   const int ntiles = static_cast<int>((end - start + kGroupTok - 1) / kGroupTok);
   if (ntiles == 0) {                              // the same for all CTAs of a cluster
