@@ -12,7 +12,8 @@ and skip the access) into _build_debug/ and compressed_attention_cvq_b200/libcvq
 which the binding loads when CVQ_LIBRARY=debug.
 
 csrc/serving_module.cpp becomes the Python module compressed_attention_cvq_b200/_serving.so
-(g++, against torch's headers): the argument checks of the serving calls.
+(g++, against torch's headers): the argument checks of the serving calls.  Where g++, Python's or
+torch's headers are missing it is left out, with a line on stderr; the library is complete without it.
 """
 from __future__ import annotations
 
@@ -93,8 +94,33 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
     return lib_path
 
 
+def _module_needs():
+    """What the Python module needs beyond the library's nvcc and this machine lacks, or None."""
+    import sysconfig
+
+    cxx = os.environ.get("CXX") or "g++"
+    if shutil.which(cxx.split()[0]) is None:
+        return f"no C++ compiler ({cxx})"
+    if not os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        return "no Python headers"
+    try:
+        import torch
+    except ImportError as e:
+        return f"no torch ({e})"
+    if not os.path.exists(os.path.join(os.path.dirname(torch.__file__), "lib", "libc10_cuda.so")):
+        return "a torch without CUDA"
+    return None
+
+
 def _build_module(force: bool, verbose: bool) -> None:
     if not force and not _stale(MODULE, MODULE_SRC):
+        return
+    lacks = _module_needs()
+    if lacks is not None:                # the C library is complete without it
+        if os.path.exists(MODULE):       # made from other sources: importing it must fail, not mislead
+            os.remove(MODULE)
+        print(f"{os.path.basename(MODULE)} not built: {lacks}. The C library does not need it; the "
+              "serving calls of the Python binding do.", file=sys.stderr)
         return
     import sysconfig
 
@@ -103,7 +129,7 @@ def _build_module(force: bool, verbose: bool) -> None:
 
     cuda = os.path.dirname(os.path.dirname(nvcc()))
     inc = [INCLUDE, *include_paths(), sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
-    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+    cmd = [*(os.environ.get("CXX") or "g++").split(), "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            *(x for d in inc for x in ("-I", d)), MODULE_SRC, "-o", MODULE,
            "-L", os.path.join(os.path.dirname(torch.__file__), "lib"), "-lc10", "-lc10_cuda",
