@@ -23,6 +23,7 @@ constexpr int kPad = kHeadDim + 4;
 // key code and value code lookups of the two layouts
 __device__ __forceinline__ int wide_code(const uint8_t* codes, const ServeArgs& a, int h, int G, int r, int t) {
   const size_t row = (static_cast<size_t>(h) * kWideGroups + G) * a.R + r;
+  if (!in_bounds(a.fault, t, a.t_cap)) return 0;
   if (a.code_bits == 6) return packed6_code(codes + row * (static_cast<size_t>(a.t_cap) / 4 * 3), t);
   return codes[row * a.t_cap + t] & 63;
 }
@@ -54,7 +55,7 @@ __device__ __forceinline__ void decode_side(const ServeArgs& a, const float* cb,
 #pragma unroll
     for (int j = 0; j < kPer * kR; ++j) {
       const int t = t0 + min(tk + j / kR * kStep, end - 1 - t0);       // t0 + 64 may pass 32 bits
-      code[j] = __ldg(codes + ((static_cast<size_t>(h) * a.t_cap + t) * kR + j % kR) * kGroups + c);
+      code[j] = in_bounds(a.fault, t, a.t_cap) ? __ldg(codes + ((static_cast<size_t>(h) * a.t_cap + t) * kR + j % kR) * kGroups + c) : 0;
     }
 #pragma unroll
     for (int j = 0; j < kPer * kR; ++j) add8(x[j / kR], cb + ((static_cast<size_t>(c) * kR + j % kR) * kCodes + code[j]) * kCodeword);
@@ -152,7 +153,7 @@ __global__ void __launch_bounds__(kThreads, RB == 16 || kWide ? 2 : 1) attend_f3
   // gathers
   auto query = [&](int i, float (&x)[8]) {
     const int r = i / 16;
-    if (r0 + r >= rows || start >= end) {
+    if (r0 + r >= rows || start >= end || !in_bounds(a.fault, grow(r), n_rows(a))) {
 #pragma unroll
       for (int d = 0; d < 8; ++d) x[d] = 0.f;
       return;
@@ -316,6 +317,7 @@ __global__ void __launch_bounds__(kThreads, RB == 16 || kWide ? 2 : 1) attend_f3
     const int r = ty * RPT + i;
     if (r0 + r >= rows) continue;
     const size_t at = grow(r) * a.n_parts + split;
+    if (!in_bounds(a.fault, at, n_part_rows(a))) continue;
     if (tx == 0) {
       a.part_m[at] = m[i];
       a.part_l[at] = l[i];
@@ -349,7 +351,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_kernel(const __grid_co
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int s = s0 + u * kMergeWarps;
-      const bool in = s < a.n_parts;
+      const bool in = s < a.n_parts && in_bounds(a.fault, row * a.n_parts + s, n_part_rows(a));
       mv[u] = in ? __ldcg(pm + s) : -INFINITY;
       lv[u] = in ? __ldcg(pl + s) : 0.f;
       x[u] = in ? __ldcg(po + static_cast<size_t>(s) * (kHeadDim / 4)) : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -388,6 +390,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge_kernel(const __grid_co
     L = fmaf(s_l[w], f, L);
     acc = make_float4(fmaf(x.x, f, acc.x), fmaf(x.y, f, acc.y), fmaf(x.z, f, acc.z), fmaf(x.w, f, acc.w));
   }
+  if (!in_bounds(a.fault, row, n_rows(a))) return;
   const float4 y = L == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(acc.x / L, acc.y / L, acc.z / L, acc.w / L);
   store_four(a.out, a.out_dtype, row * kHeadDim + 4 * lane, y);
   if (lane == 0) a.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * kLn2;

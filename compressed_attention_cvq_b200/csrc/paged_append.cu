@@ -86,7 +86,7 @@ __global__ void __launch_bounds__(kThreads, 12) paged_append_kernel(const __grid
       const int p = a.seq_lens[b] - (a.tok_offsets[b + 1] - i);
       const long long pos = (a.pos_offsets != nullptr ? a.pos_offsets[b] : 0) + static_cast<long long>(p);
       int page = -1;
-      if (p >= 0 && (p >> a.page_shift) < a.max_pages)
+      if (p >= 0 && (p >> a.page_shift) < a.max_pages && in_bounds(a.fault, b, a.batch))
         page = a.page_table[static_cast<size_t>(b) * a.max_pages + (p >> a.page_shift)];
       const int j = threadIdx.x;
       reinterpret_cast<float2*>(s_ph)[j] = phase_exact(a.phase.F[j] * static_cast<unsigned long long>(pos));
@@ -124,14 +124,16 @@ __global__ void __launch_bounds__(kThreads, 12) paged_append_kernel(const __grid
       Chunk<In, kD> out;
 #pragma unroll
       for (int d = 0; d < kD; ++d) out.x[d] = from_float<In>(x[d]);
-      *reinterpret_cast<Chunk<In, kD>*>(static_cast<In*>(a.q_out) + (static_cast<size_t>(i) * nq + r) * kHeadDim + kD * c) = out;
+      if (in_bounds(a.fault, r, a.n_q_heads) && in_bounds(a.fault, i, a.n_tokens))
+        *reinterpret_cast<Chunk<In, kD>*>(static_cast<In*>(a.q_out) + (static_cast<size_t>(i) * nq + r) * kHeadDim + kD * c) = out;
     } else if (at >= 0) {
       Kv* pool = static_cast<Kv*>(r < nk ? a.k_pages : a.v_pages);
       const int h = r < nk ? r - nq : r - nk;
       Chunk<Kv, kD> out;
 #pragma unroll
       for (int d = 0; d < kD; ++d) out.x[d] = from_float<Kv>(x[d]);
-      *reinterpret_cast<Chunk<Kv, kD>*>(pool + at + (static_cast<long long>(h) << a.page_shift) * kHeadDim + kD * c) = out;
+      if (in_bounds(a.fault, h, a.n_kv_heads) && in_bounds(a.fault, at, a.n_pages * a.page_stride))
+        *reinterpret_cast<Chunk<Kv, kD>*>(pool + at + (static_cast<long long>(h) << a.page_shift) * kHeadDim + kD * c) = out;
     }
     r += stride;
     in = next;

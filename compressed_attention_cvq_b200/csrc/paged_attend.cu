@@ -97,6 +97,7 @@ __device__ __forceinline__ uint32_t take_part<__half>(float& x, float& y) {
 // out and lse of one row from its sum (M in log2 units, L, and lane's 4 dims of o), with the
 // earlier state of the row if there is one
 __device__ __forceinline__ void finish_row(const ServeArgs& a, size_t row, int lane, float M, float L, float4 o) {
+  if (!in_bounds(a.fault, row, n_rows(a))) return;
   if (a.prev_lse != nullptr) {
     const float pz = a.prev_lse[row] * kLog2e;
     if (pz != -INFINITY) {
@@ -163,7 +164,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attend_kernel(cons
   auto token = [&](int i) { return static_cast<unsigned>(start) + static_cast<unsigned>(i) * kChunk + (lane & 15); };
   auto load_page = [&](int i) {
     const unsigned t = token(i);
-    return i < nchunks && t < static_cast<unsigned>(end) ? __ldg(table + (t >> a.page_shift)) : 0;
+    return i < nchunks && t < static_cast<unsigned>(end) && in_bounds(a.fault, t >> a.page_shift, a.max_pages)
+               ? __ldg(table + (t >> a.page_shift)) : 0;
   };
   auto issue = [&](int i, int page) {
     if (i < nchunks) {
@@ -224,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attend_kernel(cons
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int d = kt * 16 + 2 * tid + (j & 1) + (j >> 1) * 8;
-        x[kt][j] = head < a.group ? load_any(a.q, a.q_dtype, at + d) : 0.f;
+        x[kt][j] = head < a.group && in_bounds(a.fault, row0 + head, n_rows(a)) ? load_any(a.q, a.q_dtype, at + d) : 0.f;
         mx = fmaxf(mx, fabsf(x[kt][j]));
       }
     }
@@ -397,6 +399,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attend_kernel(cons
       finish_row(a, row0 + r, lane, M, sum, acc);
     } else {
       const size_t at = (row0 + r) * a.n_splits + split;
+      if (!in_bounds(a.fault, at, n_part_rows(a))) continue;
       *reinterpret_cast<float4*>(a.part_o + at * kHeadDim + 4 * lane) = acc;
       if (lane == 0) {
         a.part_m[at] = M;
@@ -408,7 +411,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attend_kernel(cons
 
   // ---- the last CTA of this (sequence, KV head) merges its splits ----
   __syncthreads();
-  int* counter = a.counters + static_cast<size_t>(b) * a.n_kv_heads + h;
+  const size_t unit = static_cast<size_t>(b) * a.n_kv_heads + h;
+  if (!in_bounds(a.fault, unit, kCounters)) return;         // the same for all threads
+  int* counter = a.counters + unit;
   if (threadIdx.x == 0) {
     int old;
     asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(old) : "l"(counter) : "memory");
@@ -433,7 +438,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) paged_attend_kernel(cons
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int s = s0 + u * W;
-        const bool in = s < used;
+        const bool in = s < used && in_bounds(a.fault, (row0 + r) * a.n_splits + s, n_part_rows(a));
         mv[u] = in ? __ldcg(pm + s) : -INFINITY;
         lv[u] = in ? __ldcg(pl + s) : 0.f;
         x[u] = in ? __ldcg(po + static_cast<size_t>(s) * (kHeadDim / 4)) : make_float4(0.f, 0.f, 0.f, 0.f);

@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(kBookThreads) prefix_book_kernel(const __grid_
     if (bits < 0x7f800000u) peak = max(peak, bits);
   }
   if (!values) x = make_float4(v[0], v[2], v[1], v[3]);
-  reinterpret_cast<float4*>(a.book)[((static_cast<size_t>(h) * C + rank) * 2 + values) * n + i] = x;
+  if (in_bounds(a.fault, i, n)) reinterpret_cast<float4*>(a.book)[((static_cast<size_t>(h) * C + rank) * 2 + values) * n + i] = x;
   peak = __reduce_max_sync(0xffffffffu, peak);
   if ((threadIdx.x & 31) == 0) warp_peak[threadIdx.x >> 5] = peak;
   __syncthreads();
@@ -396,8 +396,10 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, 1) prefix_mma_kernel(c
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (threadIdx.x < nrows) {
       const size_t at = global_row(threadIdx.x) * n_parts + blockIdx.x;
-      a.part_m[at] = -INFINITY;
-      a.part_l[at] = 0.f;
+      if (in_bounds(a.fault, at, n_part_rows(a))) {
+        a.part_m[at] = -INFINITY;
+        a.part_l[at] = 0.f;
+      }
     }
     return;
   }
@@ -456,7 +458,8 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, 1) prefix_mma_kernel(c
   // fp32 and relative to the maximum m_kept, to the workspace, and begun anew.
   float m_kept = -INFINITY;
   auto kept_row = [&](int stream, int r) {
-    return reinterpret_cast<float4*>(a.kept_o + ((global_row(min(r, nrows - 1)) * n_parts + blockIdx.x) * 2 + stream) * kHeadDim);
+    const size_t at = global_row(min(r, nrows - 1)) * n_parts + blockIdx.x;
+    return reinterpret_cast<float4*>(a.kept_o + ((in_bounds(a.fault, at, n_part_rows(a)) ? at : 0) * 2 + stream) * kHeadDim);
   };
   if (warp < kSoftWarps) {
     // ================= softmax =================
@@ -653,8 +656,12 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, 1) prefix_mma_kernel(c
       auto store = [&](int p, int u, f2 x, f2 y) {
         uint32_t l0, l1;
         const uint32_t h0 = take_half(x, l0), h1 = take_half(y, l1);
-        const uint32_t at = at0 + (kWide ? u * 128 + ((swizzle ^ u) << 4) : (p * kSlots % kTok) * 128 + (swizzle << 4));
-        const uint32_t to = kWide ? 2 * p + slot / (kTok / kRun) : p * kSlots / kTok;
+        const uint32_t tile = kKeys ? tiles_k : tiles_v;
+        uint32_t at = at0 + (kWide ? u * 128 + ((swizzle ^ u) << 4) : (p * kSlots % kTok) * 128 + (swizzle << 4));
+        uint32_t to = kWide ? 2 * p + slot / (kTok / kRun) : p * kSlots / kTok;
+        // debug build: bytes that others wait for go to a place that there is
+        if (!in_bounds(a.fault, at - tile + 7, kTile)) at = tile;
+        if (!in_bounds(a.fault, to, C)) to = rank;
         if (to == static_cast<uint32_t>(rank)) {
           sts8(at, h0, h1);
           sts8(at + kTile, l0, l1);
@@ -724,6 +731,7 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, 1) prefix_mma_kernel(c
             const uint32_t off = (p * kSlots + slot) * (packed ? 3 : 4);
             const uint32_t from = stage + (off & ~3u);
             auto word = [&](int r) {
+              if (!in_bounds(a.fault, r * Lay::kPitch + (off & ~3u) + (packed ? 7 : 3), code_bytes)) return 0u;
               const uint32_t w = lds4(from + r * Lay::kPitch);
               return packed ? __funnelshift_r(w, lds4(from + r * Lay::kPitch + 4), 8 * (off & 3)) : w;
             };
@@ -812,6 +820,8 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, 1) prefix_mma_kernel(c
         if (i >= kCodeStages && !wait(&ctl.c_empty[values][s], (i / kCodeStages - 1) & 1, a.fault)) return false;
         const long long t = start + static_cast<long long>(i) * kGroupTok;
         const int n = static_cast<int>(min(end - t, static_cast<long long>(kGroupTok)));
+        // debug build: no copy where one would leave the cache, or its stage
+        const bool fits = in_bounds(a.fault, t + n - 1, a.t_cap) && in_bounds(a.fault, (2 * s + values + 1) * code_bytes - 1, 2 * kCodeStages * code_bytes);
         unsigned char* to = smem + (ring - tiles_k) + (2 * s + values) * code_bytes;
         const uint8_t* codes = values ? a.val_codes : a.key_codes;
         if (kWide) {                              // whole pieces of 16 bytes: rows are, of either kind
@@ -819,12 +829,12 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, 1) prefix_mma_kernel(c
           const size_t row = packed ? static_cast<size_t>(a.t_cap) / 4 * 3 : static_cast<size_t>(a.t_cap);
           const uint32_t bytes = packed ? (n + 63) / 64 * 48 : (n + 15) / 16 * 16;
           const uint8_t* from = codes + (static_cast<size_t>(h) * kWideGroups + rank / (C / 2)) * rounds * row + (packed ? t / 4 * 3 : t);
-          mbar_expect_tx(full, bytes * rounds);
-          for (int r = 0; r < rounds; ++r) bulk_load(to + r * Lay::kPitch, from + r * row, bytes, full);
+          mbar_expect_tx(full, fits ? bytes * rounds : 0);
+          for (int r = 0; r < rounds && fits; ++r) bulk_load(to + r * Lay::kPitch, from + r * row, bytes, full);
         } else {
           constexpr uint32_t row = R * kGroups;
-          mbar_expect_tx(full, n * row);
-          bulk_load(to, codes + (static_cast<size_t>(h) * a.t_cap + t) * row, n * row, full);
+          mbar_expect_tx(full, fits ? n * row : 0);
+          if (fits) bulk_load(to, codes + (static_cast<size_t>(h) * a.t_cap + t) * row, n * row, full);
         }
         return true;
       };
@@ -962,16 +972,19 @@ __global__ void __launch_bounds__(Roles<kWide>::kThreads, 1) prefix_mma_kernel(c
     }
     if (st == 0 && r < nrows) {
       const size_t at = global_row(r) * n_parts + blockIdx.x;
-      a.part_m[at] = M;
-      a.part_l[at] = fmaf(l, f0, l1 * f1);
+      if (in_bounds(a.fault, at, n_part_rows(a))) {
+        a.part_m[at] = M;
+        a.part_l[at] = fmaf(l, f0, l1 * f1);
+      }
     }
   }
   tmem_before_sync();
   __syncthreads();
   for (int i = threadIdx.x; i < nrows * 32; i += kThreads) {
     const int rr = i >> 5, c = (i & 31) * 4;
-    *reinterpret_cast<float4*>(a.part_o + (global_row(rr) * n_parts + blockIdx.x) * kHeadDim + c) =
-        *reinterpret_cast<const float4*>(rows_out + rr * kOutPitch + c);
+    const size_t at = global_row(rr) * n_parts + blockIdx.x;
+    if (in_bounds(a.fault, at, n_part_rows(a)))
+      *reinterpret_cast<float4*>(a.part_o + at * kHeadDim + c) = *reinterpret_cast<const float4*>(rows_out + rr * kOutPitch + c);
   }
   if (warp == kScoreWarp)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");

@@ -11,6 +11,12 @@ namespace cvq {
 
 constexpr unsigned int kFaultPage = CVQ_PAGE_FAULT;
 
+// A workspace starts with the arrival counters of paged calls, one per (sequence, KV head), at a
+// place that no call's states reach, whatever its shape: so every paged call finds them as the last one
+// left them, at zero.  Calls of more units than that have CTAs enough without splits.
+constexpr int kCounters = 16384;
+constexpr size_t kCounterBytes = kCounters * sizeof(int);
+
 // Arguments of the attention kernels.  Split partial states are [B, Hq, n_splits] rows as in
 // the other decode kernels, with m in log2 units (the kernels work with exp2); a split with
 // no token stores m = -inf and l = 0 and leaves its o unwritten.
@@ -68,6 +74,10 @@ struct AppendArgs {
   unsigned int* fault;
   PhaseTurns phase;
 };
+
+// partial states of a call, and rows of its outputs
+__device__ __forceinline__ size_t n_part_rows(const ServeArgs& a) { return static_cast<size_t>(a.batch) * a.n_q_heads * a.n_parts; }
+__device__ __forceinline__ size_t n_rows(const ServeArgs& a) { return static_cast<size_t>(a.batch) * a.n_q_heads; }
 
 __device__ __forceinline__ float load_any(const void* p, int dtype, size_t i) {
   if (dtype == CVQ_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);

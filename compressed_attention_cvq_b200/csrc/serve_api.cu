@@ -42,12 +42,6 @@ bool prefix_on_tensor_cores(const cvq_shape* s, int q_dtype) {
   return q_dtype != CVQ_F32 && (s->t_cap >= 2048 || (s->t_cap >= 512 && rows > 64));
 }
 
-// A workspace starts with the arrival counters of paged calls, one per (sequence, KV head), at a
-// place that no call's states reach, whatever its shape: so every paged call finds them as the last one
-// left them, at zero.  Calls of more units than that have CTAs enough without splits.
-constexpr int kCounters = 16384;
-constexpr size_t kCounterBytes = kCounters * sizeof(int);
-
 // partial states of (sequence, query head) rows, 16-byte aligned
 size_t parts_bytes(int batch, int n_q_heads, int n_parts) {
   return round16(static_cast<size_t>(batch) * n_q_heads * n_parts * (kHeadDim + 2) * sizeof(float));

@@ -493,7 +493,9 @@ CVQ_API cvq_status cvq_paged_attend(const cvq_paged* paged, const void* q, int q
  *         the library (compiled with -DCVQ_DEBUG_BOUNDS, libcvq_debug.so) has these checks:
  *         the code row of every code copy, every codeword and bin index, the exchange index
  *         between the CTAs of a pair, and the partial-state rows and arrival counter of
- *         every work unit.  A failed check skips its access (a skipped load reads 0) and
+ *         every work unit; in the shared-prefix and paged calls also page-table entries, page
+ *         rows, places in operand tiles and output rows.  A failed check skips its access (a
+ *         skipped load reads 0) and
  *         the kernel runs on; the outputs of that call are then invalid.
  *         CVQ_PAGE_FAULT = a page-table entry or a token index of a paged call was out of
  *         range; the access was skipped.
