@@ -119,3 +119,32 @@ def test_tiny_queries_and_codebooks(group, R):
     got = cvq.prefix_attend(cvq.shape_of(q, dev["key_codes"], group_dim=group), q.cuda(), dev["key_cb"],
                             dev["key_codes"], dev["val_codes"], ln, dev["val_cb"], out_dtype=torch.float32)
     check(d, got, 2111)
+
+
+@pytest.mark.parametrize("t_cap", [16, 48, 272, 2064, 2096])
+@pytest.mark.parametrize("R", [1, 5, 11, 14])
+def test_capacities_of_16_tokens(t_cap, R):
+    """One-byte codes of 64-scalar groups: rows are whole pieces of 16 bytes, not of 64."""
+    for length in (t_cap, t_cap - 9):
+        d, got = run(3, 8, 2, t_cap, length, R, "fp16", 64, seed=t_cap + R)
+        check(d, got, length)
+
+
+@pytest.mark.parametrize("group,R", [(64, 14), (64, 22), (8, 2), (8, 1)])
+def test_layers_that_share_a_workspace(group, R):
+    """Calls with codebooks of their own, one after another through one workspace: rounds that are not
+    held in shared memory come from this call's codebooks."""
+    import compressed_attention_cvq_b200 as cvq
+    layers = [run(4, 8, 2, 2304, 2200, R, "bf16", group, 2, seed=s) for s in (1, 2, 3)]
+    shape = cvq.shape_of(torch.zeros(4, 8, 128), torch.from_numpy(layers[0][0]["key_codes"]), group_dim=group)
+    ws = cvq.prefix_workspace_alloc(shape, 2, "cuda")
+    ins = []
+    for d, _ in layers:
+        dev = [torch.from_numpy(d[k]).cuda() for k in ("key_cb", "key_codes", "val_codes", "val_cb")]
+        ins.append((torch.from_numpy(d["q"]).bfloat16().cuda(), dev))
+    ln = torch.tensor([2200], dtype=torch.int32, device="cuda")
+    for _ in range(3):
+        got = [cvq.prefix_attend(shape, q, kcb, kc, vc, ln, vcb, 2, workspace=ws, out_dtype=torch.float32)
+               for q, (kcb, kc, vc, vcb) in ins]
+        for (o, z), (_, (wo, wz)) in zip(got, layers):
+            assert torch.equal(o, wo) and torch.equal(z, wz)
