@@ -146,9 +146,13 @@ void raise_for(cvq_status st, const char* name) {
   throw python_error();
 }
 
-at::Tensor workspace_of(PyObject* o, size_t need, c10::Device dev, const char* what) {
+// clear: whether the call takes what the workspace holds
+at::Tensor workspace_of(PyObject* o, size_t need, c10::Device dev, const char* what, bool clear) {
   if (need == 0) bad(std::string("invalid shape or n_splits for ") + what);
-  if (o == Py_None) return at::zeros({static_cast<int64_t>(need)}, at::TensorOptions().dtype(at::kByte).device(dev));
+  if (o == Py_None) {
+    const auto bytes = at::TensorOptions().dtype(at::kByte).device(dev);
+    return clear ? at::zeros({static_cast<int64_t>(need)}, bytes) : at::empty({static_cast<int64_t>(need)}, bytes);
+  }
   const at::Tensor& ws = tensor(o, "workspace");
   if (ws.device() != dev || static_cast<size_t>(ws.numel()) * ws.element_size() < need || !ws.is_contiguous())
     bad("workspace must be " + std::to_string(need) + " dense bytes on " + dev.str());
@@ -250,7 +254,7 @@ PyObject* prefix_attend(PyObject*, PyObject* const* p, Py_ssize_t n) {
   const int qd = dtype_code(q.scalar_type(), "q");
   const On on(dev, p[12]);
   const int splits = p[7] == Py_None ? api.prefix_suggest_splits(s, qd, sm_count(dev)) : int_of(p[7]);
-  const at::Tensor ws = workspace_of(p[8], api.prefix_workspace_bytes(s, splits), dev, "cvq_prefix_workspace_bytes");
+  const at::Tensor ws = workspace_of(p[8], api.prefix_workspace_bytes(s, splits), dev, "cvq_prefix_workspace_bytes", false);
   const Outputs o = outputs_of(p[9], p[10], p[11], q.scalar_type(), s->batch, s->n_q_heads, dev);
   raise_for(api.prefix_attend(s, ptr(q), qd, ptr<float>(kcb), ks, ptr<uint8_t>(kc), ptr<uint8_t>(vc),
                               ptr<int32_t>(len), ptr<float>(vcb), vs, splits, ptr(ws), ptr(o.out),
@@ -361,7 +365,7 @@ PyObject* paged_attend(PyObject*, PyObject* const* p, Py_ssize_t n) {
   const int qd = dtype_code(q.scalar_type(), "q");
   const On on(dev, p[13]);
   const int splits = p[6] == Py_None ? api.paged_suggest_splits(g, sm_count(dev)) : int_of(p[6]);
-  const at::Tensor ws = workspace_of(p[7], api.paged_workspace_bytes(g, splits), dev, "cvq_paged_workspace_bytes");
+  const at::Tensor ws = workspace_of(p[7], api.paged_workspace_bytes(g, splits), dev, "cvq_paged_workspace_bytes", true);
   const Outputs o = outputs_of(p[10], p[11], p[12], q.scalar_type(), g->batch, g->n_q_heads, dev);
   raise_for(api.paged_attend(g, ptr(q), qd, ptr(kp), ptr(vp), ptr<int32_t>(table), ptr<int32_t>(lens),
                              splits, ptr(ws), po, pl, ptr(o.out), dtype_code(o.out.scalar_type(), "out"),

@@ -88,3 +88,26 @@ def test_a_workspace_of_its_size_is_not_left():
                           out=outs[2048:2048 + B * 1024].view(B, 8, 128))
         assert bool((big[:4096] == 0x5a).all()) and bool((big[4096 + need:] == 0x5a).all())
         assert bool((outs[:2048] == 7).all()) and bool((outs[2048 + B * 1024:] == 7).all())
+
+
+@pytest.mark.parametrize("group,R,t_cap", [(8, 1, 2304), (8, 2, 2304), (64, 12, 2304), (8, 2, 320), (8, 1, 40000)])
+def test_what_a_prefix_workspace_holds_does_not_matter(group, R, t_cap):
+    """Also through a call that makes its own, of memory that others have used."""
+    import compressed_attention_cvq_b200 as cvq
+    d = workloads.small(batch=1, n_q_heads=8, n_kv_heads=2, t_cap=t_cap, R=R, seed=R, group_dim=group)
+    dev = {k: torch.from_numpy(d[k]).cuda() for k in ("key_cb", "val_cb", "key_codes", "val_codes")}
+    x = torch.randn(5, 8, 128, device="cuda").half()
+    shape = cvq.shape_of(x, dev["key_codes"], group_dim=group)
+    ws = cvq.prefix_workspace_alloc(shape, 1, "cuda")
+
+    def call(w):
+        return cvq.prefix_attend(shape, x, dev["key_cb"], dev["key_codes"], dev["val_codes"], i32([t_cap - 5]),
+                                 dev["val_cb"], 1, workspace=w)
+    want = call(ws)
+    for byte in (0xff, 0x7f, 0x55):                          # NaN, large and small numbers
+        got = call(ws.fill_(byte))
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        used = [torch.full_like(ws, byte) for _ in range(2)]
+        del used
+        got = call(None)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
