@@ -34,10 +34,10 @@
 // token to token, 15 times at most before they are taken anew from the exact turns: each turn adds
 // an error of 2^-24, and the step's own rounding once more.
 //
-// What bounds it: the producers (fp32 sums, rotation, two parts of every number) and the products, three
+// What bounds it: the producers (fp32 sums, rotation, two parts of every number) and the products, 2.5
 // times those of one part, whose tiles have one stage: two would not fit beside the codebooks.
 // Measured in a captured graph, 32 query and 8 KV heads: 32 sequences over 131072 tokens, R = 1, 271 us
-// (three products of 68.7 GF: 760 TFLOP/s); 16 over 32768, R = 2, 93 us, and R = 11 of 64-scalar groups
+// (2.5 times 68.7 GF: 630 TFLOP/s); 16 over 32768, R = 2, 93 us, and R = 11 of 64-scalar groups
 // 218 us; a short prefix 16 us, of which the codebooks' order takes 3 and the join and merge 4.  Operands
 // of one part took 103, 42, 111 and 12 us, with outputs 3e-4 off instead of 3e-6 and lse 1e-6 instead of
 // 5e-8.

@@ -193,7 +193,7 @@ size_t cvq_paged_workspace_bytes(const cvq_paged* p, int n_splits) {
 
 int cvq_paged_suggest_splits(const cvq_paged* p, int sm_count) {
   if (check_paged(p) != CVQ_OK || sm_count < 1) return 1;
-  // A split holds 256 tokens or more (512 where there are few splits): on a window of 128 tokens one split takes 7.3 us where
+  // For sequences of like lengths.  A split holds 256 tokens or more (512 where there are few splits): on a window of 128 tokens one split takes 7.3 us where
   // two, with their merge, take 14.  Beyond that a CTA per SM carries one sequence best (131071
   // tokens: 18 splits of 8 KV heads 88.9 us, 37 splits 94.8), and of several sequences, whose
   // lengths differ, two CTAs per SM (16 sequences of 1024 to 8192: 3 splits 54.1 us, 2 64.2).

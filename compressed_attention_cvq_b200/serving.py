@@ -111,6 +111,8 @@ def make_paged(batch, n_q_heads, n_kv_heads, page_size, n_pages, max_pages,
 
 
 def paged_suggest_splits(paged, sm_count=None):
+    """A split count for sequences of like lengths; a batch with one sequence far longer than the
+    others wants that of the one alone (batch 1)."""
     return _b.lib.cvq_paged_suggest_splits(ctypes.byref(paged), _sm_count(sm_count))
 
 

@@ -374,7 +374,10 @@ CVQ_API cvq_status cvq_attend_static(const cvq_shape* shape, const void* q, int 
  *              keys and values and the softmax weights as two fp16 numbers each (22 bits), the
  *              codebooks and query rows scaled by powers of two into fp16's range; sums of codewords,
  *              rotations, sums of products, the softmax and the merge are fp32.  An output whose
- *              weighted codewords are not all finite is not finite
+ *              weighted codewords are not all finite is not finite.  The largest finite number of a
+ *              KV head's codebook, in use or not, sets its scale: numbers below 2^-17 of it keep
+ *              fewer than 22 bits, and those below 2^-39 of it count as 0.  (So no large number
+ *              as a mark of an unused codeword; one that is not finite does no harm)
  *   Errors as in cvq_attend.
  * ------------------------------------------------------------------------------- */
 CVQ_API size_t cvq_prefix_workspace_bytes(const cvq_shape* shape, int n_splits);
@@ -472,7 +475,10 @@ CVQ_API cvq_status cvq_paged_append(const cvq_paged* paged, int32_t n_tokens, co
  *   sums are kept in fp32.
  * ------------------------------------------------------------------------------- */
 CVQ_API size_t cvq_paged_workspace_bytes(const cvq_paged* paged, int n_splits);
-/* A split count for sequences of up to max_pages * page_size tokens (a suggestion). */
+/* A split count for sequences of like lengths, of up to max_pages * page_size tokens (a
+ * suggestion; it knows no lengths).  A batch with one sequence far longer than the others wants
+ * the count that this sequence would be given alone: 131072 tokens among 63 sequences of 100 take
+ * 1315 us in the one split that the batch is given, and 104 us in 18. */
 CVQ_API int cvq_paged_suggest_splits(const cvq_paged* paged, int sm_count);
 CVQ_API cvq_status cvq_paged_attend(const cvq_paged* paged, const void* q, int q_dtype,
                                     const void* k_pages, const void* v_pages,
