@@ -59,14 +59,10 @@ struct Roles {
   static constexpr int kThreads = 32 * (kCopyWarp + 1);
 };
 constexpr int kRows = 128;
-constexpr int kTok = 64;                          // tokens of a tile
 constexpr int kHalfTile = kTok * 128;             // 64 dims of one part of its keys or values, bytes
 constexpr int kTile = 2 * kHalfTile;              // one part; the second follows
 constexpr int kMostCodeStages = 4;
 constexpr int kReanchor = 2;                      // steps between exact phases
-// Tiles of a stream between flushes of its O: outputs are 3e-6 off at most (32: 7e-6, and 260 us at 131072
-// tokens where 16 takes 271).
-constexpr int kFlush = 16;
 constexpr int kOutPitch = kHeadDim + 4;           // floats; 16-byte chunks of 8 rows in 8 bank groups
 constexpr int kOutBytes = kRows * kOutPitch * 4;
 // columns of TMEM: S of the two streams (and over each, 32 scores at a time, the two parts of their

@@ -47,9 +47,12 @@ size_t parts_bytes(int batch, int n_q_heads, int n_parts) {
   return round16(static_cast<size_t>(batch) * n_q_heads * n_parts * (kHeadDim + 2) * sizeof(float));
 }
 
-// what long streams of the tensor-core kernel have summed: two outputs a row and CTA
-size_t kept_bytes(int batch, int n_q_heads, int n_parts) {
-  return static_cast<size_t>(batch) * n_q_heads * n_parts * 2 * kHeadDim * sizeof(float);
+// What long streams of the tensor-core kernel have summed: two outputs a row and CTA, where a split of a
+// full cache has more tiles than two streams sum at once.
+size_t kept_bytes(const cvq_shape* s, int n_splits) {
+  const int64_t step = kTok * prefix_cluster(s);
+  if (((static_cast<int64_t>(s->t_cap) + n_splits - 1) / n_splits + step - 1) / step <= 2 * kFlush) return 0;
+  return static_cast<size_t>(s->batch) * s->n_q_heads * n_splits * prefix_cluster(s) * 2 * kHeadDim * sizeof(float);
 }
 
 // both codebooks of every KV head
@@ -110,7 +113,7 @@ size_t cvq_prefix_workspace_bytes(const cvq_shape* s, int n_splits) {
   if (cvq_partials_bytes(s, n_splits) == 0) return 0;
   // the books' items of 16 bytes leave one peak per 256; two streams a CTA keep an output each
   const int parts = n_splits * prefix_cluster(s);
-  return kCounterBytes + parts_bytes(s->batch, s->n_q_heads, parts) + book_bytes(s) + round16(book_bytes(s) / 1024) + kept_bytes(s->batch, s->n_q_heads, parts);
+  return kCounterBytes + parts_bytes(s->batch, s->n_q_heads, parts) + book_bytes(s) + round16(book_bytes(s) / 1024) + kept_bytes(s, n_splits);
 }
 
 int cvq_prefix_suggest_splits(const cvq_shape* s, int q_dtype, int sm_count) {
